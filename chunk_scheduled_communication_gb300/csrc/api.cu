@@ -104,6 +104,20 @@ int encode_2d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, int esiz
     return SYN_OK;
 }
 
+// 3-D tiled tensor map over [rows, heads, cols] with row and head strides in
+// bytes: boxes of box_cols columns of one head, box_rows rows.
+int encode_3d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint64_t cols, uint64_t heads, uint64_t rows,
+              uint64_t head_bytes, uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz) {
+    cuuint64_t dims[3] = {cols, heads, rows};
+    cuuint64_t strides[2] = {head_bytes, row_bytes};
+    cuuint32_t box[3] = {box_cols, 1, box_rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = p_encode(m, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(SYN_ERR_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
+    return SYN_OK;
+}
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
@@ -114,6 +128,11 @@ int host_load_driver() { return load_driver(); }
 int host_encode_2d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, int esize, uint64_t cols,
                    uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz) {
     return encode_2d(m, base, dt, esize, cols, rows, box_cols, box_rows, swz);
+}
+int host_encode_3d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint64_t cols, uint64_t heads,
+                   uint64_t rows, uint64_t head_bytes, uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows,
+                   CUtensorMapSwizzle swz) {
+    return encode_3d(m, base, dt, cols, heads, rows, head_bytes, row_bytes, box_cols, box_rows, swz);
 }
 CUresult host_write32(cudaStream_t st, uint32_t *addr, uint32_t value) {
     return p_write32(reinterpret_cast<CUstream>(st), reinterpret_cast<CUdeviceptr>(addr), value,

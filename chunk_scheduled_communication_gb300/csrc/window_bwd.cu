@@ -1,0 +1,544 @@
+// window_bwd.cu -- gradient of the windowed attention (include/syn_window.h).
+//
+//   P = exp(scale S - lse),  dP = dO V^T,  dS = P * (dP - rowsum(dO * O))
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
+//
+// One kernel in two forms, so that no sum needs atomics and the bits do not
+// depend on timing: the dK, dV form keeps 128 keys and streams query blocks
+// past them (all heads of the group, so shared heads sum in the accumulator),
+// the dQ form keeps 128 query rows and streams key blocks.  The scores are
+// computed in both (seven products where five are needed); writing the score
+// gradients out for the second product instead would move T * W elements a
+// head each way.  With X, Y the stationary tiles (K, V or Q, dO) and U, W the
+// streaming ones (Q, dO or K, V), a 64-row block does
+//
+//   S = X U^T, dP = Y W^T               128 x 64 each, into TMEM buffer g & 1
+//   P, dS by the warpgroup g & 1        one stationary row per thread
+//   dV += P W (dK, dV form), dX += dS U  P and dS read from TMEM as 16-bit
+//
+//   warp 0      TMA producer: an item's X and Y, each block's U and W (ring)
+//   warp 1      MMA issuer: S, dP of block g, then the sums of block g - 1
+//   warp 2      zeroes streaming rows past the sequence's end
+//   warps 4-7, 8-11  the two warpgroups
+//
+// TMEM (512 columns): buffer b: S at 128b, dP at 128b + 64 (P and dS over
+// their first 32 columns); sums at 256 and 384.  The dQ form has one sum and
+// alternates between the two places, so an item's output is read while the
+// next item's products run.
+#include "window.cuh"
+
+namespace syn {
+namespace window {
+
+namespace {
+
+constexpr int kBX = 128, kBU = 64;
+constexpr int kBoxX = kBX * 128, kBoxU = kBU * 128;
+constexpr int kThreads = 384;
+constexpr int kStages = 4;
+
+enum {
+    B_XF = 0,                  // the item's X, Y landed
+    B_XE = 1,                  // X, Y read by the item's last S, dP
+    B_UF = 2,                  // stage landed
+    B_UE = B_UF + kStages,     // stage consumed
+    B_ZR = B_UE + kStages,     // a block with rows past the end landed
+    B_UZ = B_ZR + 1,           // its rows past the end zeroed
+    B_SF = B_UZ + 1,           // buffer b: S, dP written (2)
+    B_PF = B_SF + 2,           // buffer b: P, dS written (2)
+    B_DN = B_PF + 2,           // buffer b: sums updated (2)
+    B_OE = B_DN + 2,           // sum place read out (2)
+    B_DRAIN = B_OE + 2,
+    N_BAR = B_DRAIN + 1
+};
+
+template <int D> struct Lay {
+    static constexpr int kTileX = kBX * D * 2, kTileU = kBU * D * 2;
+    static constexpr int kStage = 2 * kTileU;
+    static constexpr int X = 0, Y = kTileX;
+    static constexpr int RING = 2 * kTileX;
+    static constexpr int STAT = RING + kStages * kStage;  // [stage][2][64] -lse2, -delta (dK, dV form)
+    static constexpr int BAR = STAT + kStages * 512;
+    static constexpr int MISC = BAR + 8 * N_BAR;
+    static constexpr int BYTES = MISC + 16 + 1024;
+};
+
+// One streaming block of an item
+struct Blk {
+    int h, start, valid;  // head; first row (of the sequence); rows that exist (64: all)
+    bool first, last;
+};
+
+template <bool KEYS> struct Walk {
+    int i, end, b, h, n;
+    const BwdItem *it;
+    __device__ __forceinline__ void load(const BwdParams &p) {
+        if (i >= end) return;
+        it = p.items + i;
+        b = 0;
+        h = it->h0;
+        // (query rows that see no key have one block without a valid row)
+        n = KEYS ? it->b1 - it->b0
+                 : max(1, (it->s_end + kBU - 1) / kBU + (it->k_end - it->w_lo + kBU - 1) / kBU);
+    }
+    __device__ __forceinline__ void init(const BwdParams &p) {
+        i = p.begin[blockIdx.x];
+        end = p.begin[blockIdx.x + 1];
+        it = p.items;
+        load(p);
+    }
+    __device__ __forceinline__ bool next(const BwdParams &p, Blk &k) {
+        if (i < end && (KEYS ? h == it->h1 : b == n)) {
+            ++i;
+            load(p);
+        }
+        if (i >= end) return false;
+        k.h = h;
+        if (KEYS) {
+            k.first = b == 0 && h == it->h0;
+            k.start = (it->b0 + b) * kBU;
+            k.valid = min(kBU, it->stream_len - k.start);
+            if (++b == n) {
+                b = 0;
+                ++h;
+            }
+            k.last = h == it->h1;
+        } else {
+            const int n_sink = (it->s_end + kBU - 1) / kBU;
+            const bool sink = b < n_sink;
+            k.first = b == 0;
+            k.start = sink ? b * kBU : it->w_lo + (b - n_sink) * kBU;
+            k.valid = min(kBU, (sink ? it->s_end : it->k_end) - k.start);
+            ++b;
+            k.last = b == n;
+        }
+        return true;
+    }
+};
+
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 96;"); }
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 200;"); }
+
+// 32 accumulator columns of this thread's row to 16-bit (dst) or fp32 (part)
+template <bool BF16>
+__device__ __forceinline__ void store_cols(uint32_t taddr, uint16_t *dst, float *part, float scale) {
+    uint32_t v[32];
+    ptx::tmem_ld_32x32b_x32(taddr, v);
+    ptx::tmem_ld_wait();
+    if (dst != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint4 o;
+            o.x = pack16<BF16>(__uint_as_float(v[8 * k + 0]) * scale, __uint_as_float(v[8 * k + 1]) * scale);
+            o.y = pack16<BF16>(__uint_as_float(v[8 * k + 2]) * scale, __uint_as_float(v[8 * k + 3]) * scale);
+            o.z = pack16<BF16>(__uint_as_float(v[8 * k + 4]) * scale, __uint_as_float(v[8 * k + 5]) * scale);
+            o.w = pack16<BF16>(__uint_as_float(v[8 * k + 6]) * scale, __uint_as_float(v[8 * k + 7]) * scale);
+            reinterpret_cast<uint4 *>(dst)[k] = o;
+        }
+    } else if (part != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            reinterpret_cast<uint4 *>(part)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    }
+}
+
+template <int D, bool BF16, bool KEYS>
+__global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_constant__ BwdParams p,
+                                                                 const __grid_constant__ BwdMaps m) {
+    using L = Lay<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = ptx::smem_u32(sm);
+    const uint32_t bar0 = sbase + L::BAR;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::MISC);
+    volatile int *abort = reinterpret_cast<volatile int *>(sm + L::MISC + 4);
+    const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    const Common &c = p.c;
+
+    if (threadIdx.x == 0) {
+        *abort = 0;
+        for (int i = 0; i < N_BAR; ++i) {
+            const bool four = i >= B_PF && i < B_PF + 2, eight = i >= B_OE && i < B_OE + 2;
+            ptx::mbar_init(bar(i), four ? 4 : eight ? 8 : 1);
+        }
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < 4) {
+        regs_dec();
+        Walk<KEYS> wk;
+        wk.init(p);
+        Blk b = {};
+        if (warp == 0) {
+            // ================= TMA producer =================
+            if (lane == 0) {
+                uint32_t g = 0, ic = 0;
+                for (; wk.next(p, b); ++g) {
+                    if (b.first) {
+                        if (!wait_bar(bar(B_XE), (ic & 1u) ^ 1u, abort, c)) break;
+                        const int hx = KEYS ? wk.it->hk : b.h;
+                        ptx::mbar_arrive_expect_tx(bar(B_XF), 2 * L::kTileX);
+                        for (int x = 0; x < D / 64; ++x) {
+                            ptx::tma_load_3d(sbase + L::X + (uint32_t)(x * kBoxX), &m.x, bar(B_XF), x * 64, hx, wk.it->row0);
+                            ptx::tma_load_3d(sbase + L::Y + (uint32_t)(x * kBoxX), &m.y, bar(B_XF), x * 64, hx, wk.it->row0);
+                        }
+                        ++ic;
+                    }
+                    const int s = (int)(g % kStages);
+                    if (!wait_bar(bar(B_UE + s), ((g / kStages) & 1u) ^ 1u, abort, c)) break;
+                    const uint32_t u = sbase + (uint32_t)(L::RING + s * L::kStage);
+                    const int hu = KEYS ? b.h : wk.it->hk, row = wk.it->stream0 + b.start;
+                    ptx::mbar_arrive_expect_tx(bar(B_UF + s), L::kStage + (KEYS ? 512 : 0));
+                    for (int x = 0; x < D / 64; ++x) {
+                        ptx::tma_load_3d(u + (uint32_t)(x * kBoxU), &m.u, bar(B_UF + s), x * 64, hu, row);
+                        ptx::tma_load_3d(u + (uint32_t)(L::kTileU + x * kBoxU), &m.w, bar(B_UF + s), x * 64, hu, row);
+                    }
+                    if (KEYS) {  // the block's statistics: 64 rows, aligned in the padded layout
+                        const int64_t o = (int64_t)b.h * p.pad_rows + wk.it->pad_row0 + b.start;
+                        ptx::bulk_g2s(sbase + (uint32_t)(L::STAT + s * 512), p.nlse2 + o, 256, bar(B_UF + s));
+                        ptx::bulk_g2s(sbase + (uint32_t)(L::STAT + s * 512 + 256), p.ndelta + o, 256, bar(B_UF + s));
+                    }
+                }
+                // every load issued must land before the CTA exits
+                if (ic > 0) drain_bar(bar(B_XF), (ic - 1u) & 1u, c);
+                for (uint32_t s = 0; s < kStages; ++s)
+                    if (g > s) drain_bar(bar(B_UF + (int)s), ((g - 1u - s) / kStages) & 1u, c);
+            }
+        } else if (warp == 2) {
+            // ================= streaming rows past the end =================
+            // (asked by the issuer, which follows every block: this warp sees only
+            // some, and a phase of the stage's own barrier could pass it by)
+            uint32_t nz = 0;
+            for (uint32_t g = 0; wk.next(p, b); ++g) {
+                if (b.valid >= kBU) continue;
+                const int s = (int)(g % kStages);
+                const bool w = wait_bar(bar(B_ZR), nz++ & 1u, abort, c);
+                if (!__all_sync(0xffffffffu, w)) break;
+                zero_rows<D>(sm + L::RING + s * L::kStage, kBoxU, b.valid, kBU, lane);
+                zero_rows<D>(sm + L::RING + s * L::kStage + L::kTileU, kBoxU, b.valid, kBU, lane);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(B_UZ));
+            }
+        } else if (warp == 1) {
+            // ================= MMA issuer =================
+            if (lane == 0) {
+                constexpr uint32_t id_s = ptx::idesc_16bit_f32(BF16, 128, kBU, false);
+                constexpr uint32_t id_a = ptx::idesc_16bit_f32(BF16, 128, D, true);
+                uint32_t nz = 0, ic = 0;
+                // sums of block g: dX (+)= dS U, and dY (+)= P W in the dK, dV form
+                auto sums = [&](uint32_t g, const Blk &k, uint32_t item) -> bool {
+                    const int s = (int)(g % kStages);
+                    const uint32_t buf = tmem + (g & 1u) * 128u;
+                    if (!wait_bar(bar(B_PF + (int)(g & 1u)), (g >> 1) & 1u, abort, c)) return false;
+                    if (k.first) {  // the place's previous output has been read
+                        const bool w = KEYS ? item == 0 || wait_bar(bar(B_OE), (item - 1u) & 1u, abort, c)
+                                            : item < 2 || wait_bar(bar(B_OE + (int)(item & 1u)), ((item >> 1) - 1u) & 1u, abort, c);
+                        if (!w) return false;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t u = sbase + (uint32_t)(L::RING + s * L::kStage);
+                    const uint32_t dx = tmem + 256u + (KEYS ? 0u : (item & 1u) * 128u);
+#pragma unroll
+                    for (int kk = 0; kk < kBU / 16; ++kk) {
+                        const uint32_t acc = (kk != 0 || !k.first) ? 1u : 0u;
+                        if (KEYS)
+                            ptx::umma_bf16_ts(tmem + 384u, buf + (uint32_t)(kk * 8), mnmajor_desc(u + L::kTileU, kBoxU, kk), id_a, acc);
+                        ptx::umma_bf16_ts(dx, buf + 64u + (uint32_t)(kk * 8), mnmajor_desc(u, kBoxU, kk), id_a, acc);
+                    }
+                    ptx::umma_commit(bar(B_DN + (int)(g & 1u)));
+                    ptx::umma_commit(bar(B_UE + s));
+                    return true;
+                };
+                Blk prev = {};
+                uint32_t g = 0;
+                bool ok = true;
+                for (; ok && wk.next(p, b); ++g) {
+                    if (b.first) {
+                        if (!wait_bar(bar(B_XF), ic & 1u, abort, c)) { ok = false; break; }
+                        ++ic;
+                    }
+                    const int s = (int)(g % kStages);
+                    if (!wait_bar(bar(B_UF + s), (g / kStages) & 1u, abort, c)) { ok = false; break; }
+                    if (b.valid < kBU) {
+                        ptx::mbar_arrive(bar(B_ZR));
+                        if (!wait_bar(bar(B_UZ), nz & 1u, abort, c)) { ok = false; break; }
+                        ++nz;
+                    }
+                    // buffer g & 1: P, dS of block g - 2 read
+                    if (g > 1 && !wait_bar(bar(B_DN + (int)(g & 1u)), ((g >> 1) - 1u) & 1u, abort, c)) { ok = false; break; }
+                    ptx::tc_fence_after();
+                    const uint32_t u = sbase + (uint32_t)(L::RING + s * L::kStage);
+                    const uint32_t buf = tmem + (g & 1u) * 128u;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        ptx::umma_bf16(buf, kmajor_desc(sbase + L::X, kBoxX, kk), kmajor_desc(u, kBoxU, kk), id_s, kk != 0 ? 1u : 0u);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        ptx::umma_bf16(buf + 64u, kmajor_desc(sbase + L::Y, kBoxX, kk), kmajor_desc(u + L::kTileU, kBoxU, kk), id_s,
+                                       kk != 0 ? 1u : 0u);
+                    ptx::umma_commit(bar(B_SF + (int)(g & 1u)));
+                    if (b.last) ptx::umma_commit(bar(B_XE));
+                    if (g > 0) ok = sums(g - 1u, prev, b.first ? ic - 2u : ic - 1u);
+                    prev = b;
+                }
+                if (ok && g > 0) sums(g - 1u, prev, ic - 1u);
+                // every MMA issued must complete before TMEM is released
+                ptx::umma_commit(bar(B_DRAIN));
+                drain_bar(bar(B_DRAIN), 0, c);
+            }
+        }
+    } else {
+        regs_inc();
+        // ================= P and dS of the warpgroup's blocks; the items' outputs =================
+        const int wg = (warp - 4) >> 2;
+        const int qd = warp & 3;
+        const int row = qd * 32 + lane;
+        const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
+        const uint32_t ts = tl + (uint32_t)(wg * 128);
+        const uint64_t scale2 = f2(c.scale_log2, c.scale_log2);
+        Walk<KEYS> wk;
+        wk.init(p);
+        Blk b = {};
+        uint32_t item = 0;
+        float nl = 0.f, nd = 0.f;  // dQ form: the row's -lse2, -delta
+        for (uint32_t g = 0; wk.next(p, b); ++g) {
+            const BwdItem &it = *wk.it;
+            if (!KEYS && b.first) {
+                const bool mine = row < it.n_rows;
+                const int64_t o = (int64_t)b.h * p.pad_rows + it.pad_row0 + (mine ? row : 0);
+                nl = mine ? p.nlse2[o] : -INFINITY;
+                nd = mine ? p.ndelta[o] : 0.f;
+            }
+            if ((g & 1u) == (uint32_t)wg) {
+                const int s = (int)(g % kStages);
+                bool w = wait_bar(bar(B_SF + wg), (g >> 1) & 1u, abort, c);
+                if (KEYS) w = w && wait_bar(bar(B_UF + s), (g / kStages) & 1u, abort, c);  // the statistics
+                if (!__all_sync(0xffffffffu, w)) break;
+                ptx::tc_fence_after();
+                uint32_t sv[64], dv[64];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    ptx::tmem_ld_32x32b_x32(ts + (uint32_t)(x * 32), *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * x));
+                    ptx::tmem_ld_32x32b_x32(ts + 64u + (uint32_t)(x * 32), *reinterpret_cast<uint32_t(*)[32]>(dv + 32 * x));
+                }
+                ptx::tmem_ld_wait();
+                // columns [lo, hi) and those below sk are seen
+                const int pos = it.pos0 + row;
+                int lo, hi, sk = 0;
+                bool masked;
+                if (KEYS) {  // a key's row over query positions
+                    const int p0 = it.off + b.start;
+                    lo = clampi(pos - p0, 0, kBU);
+                    hi = pos < c.sinks ? kBU : clampi(pos + c.window - p0, 0, kBU);
+                    masked = p0 < it.pos0 + kBX - 1 || (it.pos0 <= p0 + kBU - 1 - c.window && it.pos0 + kBX > c.sinks);
+                } else {     // a query's row over keys
+                    hi = clampi(min(b.start + b.valid, pos + 1) - b.start, 0, kBU);
+                    lo = clampi(pos - c.window + 1 - b.start, 0, kBU);
+                    sk = clampi(c.sinks - b.start, 0, kBU);
+                    masked = b.valid < kBU || b.start + kBU - 1 > it.pos0 ||
+                             (b.start <= it.pos0 + kBX - 1 - c.window && b.start + kBU > c.sinks);
+                }
+                const float4 *st_l = reinterpret_cast<const float4 *>(sm + L::STAT + s * 512);
+                uint32_t pk[32], dk[32];
+#pragma unroll
+                for (int k = 0; k < kBU; k += 4) {
+                    float4 a, d;
+                    if (KEYS) {
+                        a = st_l[k / 4];
+                        d = st_l[16 + k / 4];
+                    } else {
+                        a = make_float4(nl, nl, nl, nl);
+                        d = make_float4(nd, nd, nd, nd);
+                    }
+                    float x0, x1, x2, x3, y0, y1, y2, y3;
+                    unf2(fma2(f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), scale2, f2(a.x, a.y)), x0, x1);
+                    unf2(fma2(f2(__uint_as_float(sv[k + 2]), __uint_as_float(sv[k + 3])), scale2, f2(a.z, a.w)), x2, x3);
+                    float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
+                    unf2(mul2(f2(p0, p1), add2(f2(__uint_as_float(dv[k]), __uint_as_float(dv[k + 1])), f2(d.x, d.y))), y0, y1);
+                    unf2(mul2(f2(p2, p3), add2(f2(__uint_as_float(dv[k + 2]), __uint_as_float(dv[k + 3])), f2(d.z, d.w))), y2, y3);
+                    if (masked) {
+                        const bool n0 = k >= hi || (k < lo && k >= sk), n1 = k + 1 >= hi || (k + 1 < lo && k + 1 >= sk);
+                        const bool n2 = k + 2 >= hi || (k + 2 < lo && k + 2 >= sk), n3 = k + 3 >= hi || (k + 3 < lo && k + 3 >= sk);
+                        if (n0) p0 = y0 = 0.f;
+                        if (n1) p1 = y1 = 0.f;
+                        if (n2) p2 = y2 = 0.f;
+                        if (n3) p3 = y3 = 0.f;
+                    }
+                    pk[k / 2] = pack16<BF16>(p0, p1);
+                    pk[k / 2 + 1] = pack16<BF16>(p2, p3);
+                    dk[k / 2] = pack16<BF16>(y0, y1);
+                    dk[k / 2 + 1] = pack16<BF16>(y2, y3);
+                }
+                if (KEYS) ptx::tmem_st_32x32b_x32(ts, pk);
+                ptx::tmem_st_32x32b_x32(ts + 64u, dk);
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(B_PF + wg));
+            }
+            if (b.last) {  // the item's sums are complete
+                const bool w = wait_bar(bar(B_DN + (int)(g & 1u)), (g >> 1) & 1u, abort, c);
+                if (!__all_sync(0xffffffffu, w)) break;
+                ptx::tc_fence_after();
+                const bool mine = row < it.n_rows;
+                const int64_t r = it.row0 + row;
+                if (KEYS) {  // warpgroup 0 writes dK, warpgroup 1 dV
+                    const Out &o = wg == 0 ? p.dx : p.dy;
+                    uint16_t *dst = nullptr;
+                    float *part = nullptr;
+                    if (it.part >= 0) part = p.part + (((int64_t)it.part * 2 + wg) * kBX + row) * D;
+                    else if (mine) dst = static_cast<uint16_t *>(o.p) + r * o.token + it.hk * o.head;
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x)
+                        store_cols<BF16>(tl + 256u + (uint32_t)(wg * 128 + x * 32), dst ? dst + x * 32 : nullptr,
+                                         part ? part + x * 32 : nullptr, wg == 0 ? c.scale : 1.f);
+                } else {     // each warpgroup half of dQ's columns
+                    uint16_t *dst = mine ? static_cast<uint16_t *>(p.dx.p) + r * p.dx.token + b.h * p.dx.head + wg * (D / 2) : nullptr;
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x)
+                        store_cols<BF16>(tl + 256u + (item & 1u) * 128u + (uint32_t)(wg * (D / 2) + x * 32),
+                                         dst ? dst + x * 32 : nullptr, nullptr, c.scale);
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(B_OE + (KEYS ? 0 : (int)(item & 1u))));
+                ++item;
+            }
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// -lse log2(e) and -rowsum(dO * O) of each row and head into [head][padded row],
+// so that a block's 64 statistics are one aligned run.  Eight lanes a row.
+template <bool BF16> __global__ void __launch_bounds__(256) window_prep_kernel(const __grid_constant__ PrepParams p) {
+    const PrepTile t = p.tiles[blockIdx.x];
+    const int sub = (int)threadIdx.x & 7, grp = (int)threadIdx.x >> 3;
+    const uint32_t mask = 0xffu << (threadIdx.x & 24u);
+    for (int i = (int)blockIdx.y * 32 + grp; i < 64 * p.H_q; i += (int)gridDim.y * 32) {
+        const int r = i / p.H_q, h = i - r * p.H_q;
+        float v = 0.f, nl = -INFINITY;
+        if (r < t.n_rows) {
+            const int64_t row = t.row0 + r;
+            const uint16_t *a = static_cast<const uint16_t *>(p.o) + row * p.o_token + h * p.o_head;
+            const uint16_t *b = static_cast<const uint16_t *>(p.d_o) + row * p.do_token + h * p.do_head;
+            const float l = p.lse[row * p.H_q + h];
+            if (l != -INFINITY) {
+                nl = -l * 1.4426950408889634f;
+                for (int k = sub * 8; k < p.d; k += 64) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(a + k), y = *reinterpret_cast<const uint4 *>(b + k);
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float2 u, w;
+                        if (BF16) {
+                            u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&xs[j]));
+                            w = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&ys[j]));
+                        } else {
+                            u = __half22float2(*reinterpret_cast<const __half2 *>(&xs[j]));
+                            w = __half22float2(*reinterpret_cast<const __half2 *>(&ys[j]));
+                        }
+                        v = fmaf(u.x, w.x, fmaf(u.y, w.y, v));
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(mask, v, o);
+        if (sub == 0) {
+            const int64_t at = (int64_t)h * p.pad_rows + t.pad_row0 + r;
+            p.nlse2[at] = nl;
+            p.ndelta[at] = -v;
+        }
+    }
+}
+
+// dK, dV tiles that were summed in parts: the parts in their fixed order
+template <bool BF16> __global__ void __launch_bounds__(256) window_sum_kernel(const __grid_constant__ SumParams p) {
+    const SumItem it = p.items[blockIdx.x];
+    const int per = p.d / 8;
+    for (int i = (int)threadIdx.x; i < it.n_rows * per; i += 256) {
+        const int r = i / per, k = (i - r * per) * 8;
+        float v[8] = {};
+        for (int j = 0; j < it.n_parts; ++j) {
+            const float4 *src = reinterpret_cast<const float4 *>(
+                p.part + (((int64_t)(it.part0 + j) * 2 + blockIdx.y) * kBX + r) * p.d + k);
+            const float4 a = src[0], b = src[1];
+            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+            v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+        }
+        const float s = blockIdx.y == 0 ? p.scale : 1.f;
+        const Out &o = blockIdx.y == 0 ? p.dk : p.dv;
+        uint4 w;
+        w.x = pack16<BF16>(v[0] * s, v[1] * s);
+        w.y = pack16<BF16>(v[2] * s, v[3] * s);
+        w.z = pack16<BF16>(v[4] * s, v[5] * s);
+        w.w = pack16<BF16>(v[6] * s, v[7] * s);
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(o.p) + (it.row0 + r) * o.token + it.hk * o.head + k) = w;
+    }
+}
+
+template <int D, bool BF16, bool KEYS>
+cudaError_t launch(int grid, const BwdParams &p, const BwdMaps &m, cudaStream_t st) {
+    window_bwd_kernel<D, BF16, KEYS><<<grid, kThreads, Lay<D>::BYTES, st>>>(p, m);
+    return cudaGetLastError();
+}
+template <int D, bool BF16> cudaError_t prepare() {
+    cudaError_t e = cudaFuncSetAttribute(window_bwd_kernel<D, BF16, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Lay<D>::BYTES);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(window_bwd_kernel<D, BF16, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Lay<D>::BYTES);
+}
+
+}  // namespace
+
+int bwd_smem(int d) { return d == 64 ? Lay<64>::BYTES : Lay<128>::BYTES; }
+
+cudaError_t bwd_prepare(int d, bool bf16) {
+    if (d == 64) return bf16 ? prepare<64, true>() : prepare<64, false>();
+    return bf16 ? prepare<128, true>() : prepare<128, false>();
+}
+
+cudaError_t bwd_launch(int d, bool bf16, bool keys, int grid, const BwdParams &p, const BwdMaps &m, cudaStream_t st) {
+    if (d == 64) {
+        if (bf16) return keys ? launch<64, true, true>(grid, p, m, st) : launch<64, true, false>(grid, p, m, st);
+        return keys ? launch<64, false, true>(grid, p, m, st) : launch<64, false, false>(grid, p, m, st);
+    }
+    if (bf16) return keys ? launch<128, true, true>(grid, p, m, st) : launch<128, true, false>(grid, p, m, st);
+    return keys ? launch<128, false, true>(grid, p, m, st) : launch<128, false, false>(grid, p, m, st);
+}
+
+cudaError_t bwd_prep_launch(bool bf16, int n_tiles, const PrepParams &p, cudaStream_t st) {
+    // a block takes up to 8 rows of heads per group of lanes
+    const dim3 grid((unsigned)n_tiles, (unsigned)((64 * p.H_q + 255) / 256));
+    if (bf16) window_prep_kernel<true><<<grid, 256, 0, st>>>(p);
+    else window_prep_kernel<false><<<grid, 256, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t bwd_sum_launch(bool bf16, int n_items, const SumParams &p, cudaStream_t st) {
+    const dim3 grid((unsigned)n_items, 2);
+    if (bf16) window_sum_kernel<true><<<grid, 256, 0, st>>>(p);
+    else window_sum_kernel<false><<<grid, 256, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace window
+}  // namespace syn
