@@ -47,7 +47,8 @@ enum {
     B_SF = B_UZ + 1,           // buffer b: S, dP written (2)
     B_PF = B_SF + 2,           // buffer b: P, dS written (2)
     B_DN = B_PF + 2,           // buffer b: sums updated (2)
-    B_OE = B_DN + 2,           // sum place read out (2)
+    B_AF = B_DN + 2,           // an item's sums complete
+    B_OE = B_AF + 1,           // sum place read out (2)
     B_DRAIN = B_OE + 2,
     N_BAR = B_DRAIN + 1
 };
@@ -258,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
                     }
                     ptx::umma_commit(bar(B_DN + (int)(g & 1u)));
                     ptx::umma_commit(bar(B_UE + s));
+                    if (k.last) ptx::umma_commit(bar(B_AF));
                     return true;
                 };
                 Blk prev = {};
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
                 if (lane == 0) ptx::mbar_arrive(bar(B_PF + wg));
             }
             if (b.last) {  // the item's sums are complete
-                const bool w = wait_bar(bar(B_DN + (int)(g & 1u)), (g >> 1) & 1u, abort, c);
+                const bool w = wait_bar(bar(B_AF), item & 1u, abort, c);
                 if (!__all_sync(0xffffffffu, w)) break;
                 ptx::tc_fence_after();
                 const bool mine = row < it.n_rows;
