@@ -5,8 +5,10 @@
 // heads only, so HBM bounds a full batch and latency a small one.  A CTA takes
 // one sequence, one kv head, up to 16 of its query heads and one of `splits`
 // ranges of the visible keys (the sinks and the window as one index space), 64
-// keys a tile: cp.async brings tiles ahead into a ring, each of four warps
-// takes 16 of a tile's keys with a running maximum and sum of its own
+// keys a tile.  Each of 128 threads resolves the page of one K or V row of a
+// tile ahead and brings the row into a ring with one bulk copy (rows 16 bytes
+// apart from their length, so that ldmatrix meets no bank twice); each of four
+// warps takes 16 of a tile's keys with a running maximum and sum of its own
 // (mma.sync 16 x 8 x 16: a group's few rows could not fill a tcgen05 tile, and
 // the tensor pipe is far from the bound).  The warps join through shared
 // memory, the ranges through a workspace in the CTA that arrives last, in the
@@ -41,8 +43,10 @@ struct DecParams {
     int64_t k_page, k_token, k_head, v_page, v_token, v_head;
     const int32_t *table, *lens;
     int64_t table_stride, n_pages, cap;  // cap: keys a sequence's table can name
-    int32_t page_size, window, sinks, H_q, H_kv, G, hgroups, splits;
+    int32_t page_size, page_shift;  // page_shift: log2(page_size), -1: not a power of two
+    int32_t window, sinks, H_q, H_kv, G, hgroups, splits;
     float scale_log2;
+    uint64_t timeout_ns;
     void *o;
     float *lse;
     float *part;        // [slot][split][16 * (D + 2)]: O, m, l
@@ -51,13 +55,6 @@ struct DecParams {
 };
 
 namespace {
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool real) {
-    const int n = real ? 16 : 0;  // 0: the 16 bytes are zeroed
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -80,11 +77,13 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 }
 
 template <int D> struct DecLay {
-    static constexpr int kTile = kTileKeys * D * 2;
-    static constexpr int RING = 0;                                  // [stage][K, V]
-    static constexpr int VALID = RING + kDecStages * 2 * kTile;     // [stage][64] key can be read
+    static constexpr int kRow = D * 2 + 16;
+    static constexpr int kTile = kTileKeys * kRow;
+    static constexpr int RING = 0;                                    // [stage][K, V]
+    static constexpr int VALID = RING + kDecStages * 2 * kTile;       // [stage][64] key can be read
     static constexpr int MERGE = VALID + kDecStages * kTileKeys * 4;  // [4][16] m, [4][16] l
-    static constexpr int BYTES = MERGE + 2 * 4 * kRowsM * 4 + 16;
+    static constexpr int BAR = MERGE + 2 * 4 * kRowsM * 4;            // a stage's rows landed
+    static constexpr int BYTES = BAR + 8 * kDecStages;
 };
 
 template <int D, bool BF16>
@@ -129,35 +128,59 @@ __global__ void __launch_bounds__(kDecThreads) window_decode_kernel(const __grid
 
     const uint32_t sbase = ptx::smem_u32(sm);
     int *valid = reinterpret_cast<int *>(sm + L::VALID);
-    constexpr int kChunks = D / 8, kRowStep = kDecThreads / kChunks;
-    const int chunk = (int)threadIdx.x % kChunks, row0 = (int)threadIdx.x / kChunks;
-    auto load = [&](int tile, int st) {
-        const uint32_t kd = sbase + (uint32_t)(L::RING + st * 2 * L::kTile), vd = kd + L::kTile;
+    auto bar = [&](int st) { return sbase + (uint32_t)(L::BAR + 8 * st); };
+    if (threadIdx.x == 0) {
+        for (int st = 0; st < kDecStages; ++st) ptx::mbar_init(bar(st), kDecThreads);
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    // thread: row `r` of a tile's keys (threads 0-63) or values (64-127)
+    const int r = (int)threadIdx.x & 63;
+    const bool is_v = threadIdx.x >= 64;
+    const uint16_t *cache = static_cast<const uint16_t *>(is_v ? p.v : p.k) + hk * (is_v ? p.v_head : p.k_head);
+    const int64_t page_stride = is_v ? p.v_page : p.k_page, token_stride = is_v ? p.v_token : p.k_token;
+    const int32_t *table = p.table != nullptr ? p.table + (int64_t)s * p.table_stride : nullptr;
+    // the row's key in a tile, -1 past the last visible one
+    auto key_of = [&](int tile) {
+        const int i = tile * kTileKeys + r;
+        return i >= n_vis ? -1 : i < s_end ? i : w_lo + (i - s_end);
+    };
+    auto page_of = [&](int j) { return p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size; };
+    // the page that holds a key: -1 no key, -2 out of range
+    auto lookup = [&](int tile) -> int {
+        const int j = tile < t1 ? key_of(tile) : -1;
+        if (j < 0) return -1;
+        if (j >= p.cap) return -2;
+        return table != nullptr ? table[page_of(j)] : s;
+    };
+    auto load = [&](int tile, int st, int page) {
+        uint8_t *dst = sm + L::RING + (st * 2 + (is_v ? 1 : 0)) * L::kTile + r * L::kRow;
+        bool real = page >= 0 && page < p.n_pages;
+        if (!real && page != -1) atomicCAS(p.err, 0, SYN_ERR_BOUNDS);
+        if (!is_v) valid[st * kTileKeys + r] = real;
+        if (real) {
+            const int j = key_of(tile), at = j - page_of(j) * p.page_size;
+            ptx::mbar_arrive_expect_tx(bar(st), D * 2);
+            ptx::bulk_g2s(ptx::smem_u32(dst), cache + page * page_stride + at * token_stride, D * 2, bar(st));
+        } else {
 #pragma unroll
-        for (int n = 0; n < kTileKeys / kRowStep; ++n) {
-            const int r = row0 + n * kRowStep;
-            const int i = tile * kTileKeys + r;
-            const int j = i < s_end ? i : w_lo + (i - s_end);
-            bool real = i < n_vis;
-            int64_t page = 0;
-            int at = 0;
-            if (real) {
-                const int e = j / p.page_size;
-                at = j - e * p.page_size;
-                real = j < p.cap;
-                if (real) {
-                    page = p.table != nullptr ? p.table[(int64_t)s * p.table_stride + e] : s;
-                    real = page >= 0 && page < p.n_pages;
-                }
-                if (!real) atomicCAS(p.err, 0, SYN_ERR_BOUNDS);
-            }
-            if (!real) page = at = 0;
-            const uint32_t off = (uint32_t)(r * D * 2 + ((chunk ^ (r & 7)) * 16));
-            cp16(kd + off, static_cast<const uint16_t *>(p.k) + page * p.k_page + at * p.k_token + hk * p.k_head + chunk * 8, real);
-            cp16(vd + off, static_cast<const uint16_t *>(p.v) + page * p.v_page + at * p.v_token + hk * p.v_head + chunk * 8, real);
-            if (chunk == 0) valid[st * kTileKeys + r] = real;
+            for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4 *>(dst)[c] = make_uint4(0, 0, 0, 0);
+            ptx::mbar_arrive(bar(st));
         }
     };
+    // the rows of the stage landed; bounded
+    auto landed = [&](int st, uint32_t parity) {
+        if (ptx::mbar_try_wait(bar(st), parity)) return true;
+        const uint64_t begin = ptx::globaltimer();
+        while (!ptx::mbar_try_wait(bar(st), parity))
+            if (ptx::globaltimer() - begin > p.timeout_ns) {
+                atomicCAS(p.err, 0, SYN_ERR_TIMEOUT);
+                return false;
+            }
+        return true;
+    };
+    int page = lookup(t0);
+    __syncthreads();  // the barriers are initialised
 
     float o[D / 8][4];
 #pragma unroll
@@ -166,26 +189,25 @@ __global__ void __launch_bounds__(kDecThreads) window_decode_kernel(const __grid
         for (int x = 0; x < 4; ++x) o[n][x] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g and g + 8
 
-#pragma unroll
     for (int x = 0; x < kDecStages - 1; ++x) {
-        if (t0 + x < t1) load(t0 + x, x);
-        cp_commit();
+        if (t0 + x < t1) load(t0 + x, x, page);
+        page = lookup(t0 + x + 1);
     }
     for (int t = t0; t < t1; ++t) {
         const int st = (t - t0) % kDecStages;
-        cp_wait<kDecStages - 2>();
-        __syncthreads();  // the tile is here, and the stage read last is free
-        if (t + kDecStages - 1 < t1) load(t + kDecStages - 1, (t - t0 + kDecStages - 1) % kDecStages);
-        cp_commit();
+        if (t > t0) __syncthreads();  // the stage read last is free
+        if (t + kDecStages - 1 < t1) load(t + kDecStages - 1, (t - t0 + kDecStages - 1) % kDecStages, page);
+        page = lookup(t + kDecStages);
+        landed(st, (uint32_t)((t - t0) / kDecStages) & 1u);
         const uint32_t kd = sbase + (uint32_t)(L::RING + st * 2 * L::kTile), vd = kd + L::kTile;
         float sc[2][4] = {};
         {
-            const int r = warp * 16 + (lane >> 4) * 8 + (lane & 7);
+            const int row = warp * 16 + (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 uint32_t b[4];
                 const int c = 2 * kk + ((lane >> 3) & 1);
-                ldsm(b, kd + (uint32_t)(r * D * 2 + ((c ^ (r & 7)) * 16)));
+                ldsm(b, kd + (uint32_t)(row * L::kRow + c * 16));
                 mma<BF16>(sc[0], qf[kk], b[0], b[1]);
                 mma<BF16>(sc[1], qf[kk], b[2], b[3]);
             }
@@ -229,12 +251,12 @@ __global__ void __launch_bounds__(kDecThreads) window_decode_kernel(const __grid
             pf[2 * n + 1] = pack16<BF16>(e[2], e[3]);
         }
         {
-            const int r = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+            const int row = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
 #pragma unroll
             for (int nn = 0; nn < D / 16; ++nn) {
                 uint32_t b[4];
                 const int c = 2 * nn + (lane >> 4);
-                ldsm_t(b, vd + (uint32_t)(r * D * 2 + ((c ^ (r & 7)) * 16)));
+                ldsm_t(b, vd + (uint32_t)(row * L::kRow + c * 16));
                 mma<BF16>(o[2 * nn], pf, b[0], b[1]);
                 mma<BF16>(o[2 * nn + 1], pf, b[2], b[3]);
             }
@@ -245,7 +267,6 @@ __global__ void __launch_bounds__(kDecThreads) window_decode_kernel(const __grid
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
     }
-    cp_wait<0>();
     __syncthreads();
     // join the warps: O of each scaled to the common maximum, in the ring's memory
     float *mm = reinterpret_cast<float *>(sm + L::MERGE), *ll = mm + 4 * kRowsM;
@@ -502,6 +523,10 @@ int syn_window_decode(syn_decode_plan_t pl, const syn_window_rows_t *q, const sy
     p.part = pl->d_part;
     p.arrived = pl->d_arrived;
     p.err = pl->d_err;
+    p.timeout_ns = host_timeout_ns();
+    p.page_shift = -1;
+    for (int b = 0; b < 31; ++b)
+        if (c.page_size == 1 << b) p.page_shift = b;
     // Ranges: enough CTAs for kWaves rounds of the resident ones, but ranges of
     // no less than kMinTiles tiles of the longest sequence the table allows.
     const int64_t n = (int64_t)n_seqs * c.H_kv * pl->hgroups;

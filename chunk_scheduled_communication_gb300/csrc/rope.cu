@@ -6,9 +6,10 @@
 // launch at a token.  A head (row) belongs to a group of L lanes; a lane holds
 // one slot of the row: 2 * VEC elements as two 16-byte vectors that contain
 // both members of each of its VEC pairs, so that the turn needs no exchange
-// between lanes and the norm's sum one shuffle tree over L lanes.  A group
-// takes a unit of up to `rows` heads of one token, computes the unit's cosines
-// and sines once into registers and walks the heads.
+// between lanes and the norm's sum one shuffle tree over L lanes.  A block
+// takes a few tokens with all their heads: its threads issue the loads of their
+// first rows, compute the tokens' cosines and sines into shared memory while
+// these are under way, and then walk the rows, tensor by tensor.
 //
 // The angle of position p and frequency f is p * f mod 2 pi.  f / 2 pi is kept
 // as a 64-bit fraction of a turn; the 64-bit product with p drops whole turns
@@ -26,32 +27,38 @@
 #include "host_util.h"
 #include "syn.h"
 #include "syn_rope.h"
+#include "window.cuh"
 
 namespace syn {
 namespace rope {
 
 constexpr int kThreads = 256;
 constexpr int kMaxD = 256;
-constexpr int kRows = 8;            // heads that share one computation of the angles
+constexpr int kRowsPerLane = 4;     // rows whose loads a lane has under way at long inputs (gradient: half)
 constexpr int kBlocksPerSm = 4;
+constexpr int kGradBlocksPerSm = 2; // persistent blocks of the gradient kernel
+constexpr int kTableBytes = 14 * 1024;  // cosines and sines of a block's tokens at most
 
 struct Tensor {
     const void *x, *dy;  // dy: the gradient kernel only
     void *y;             // the gradient kernel: dx
     int64_t xt, xh, gt, gh, yt, yh;
     const void *w;
-    int32_t heads, splits;
+    int32_t heads;
+    uint32_t magic, shift;  // r / heads = r * magic >> shift
     int32_t copy, scatter, norm;
 };
 
 struct Args {
     Tensor t[3];
-    int32_t n_tensors, rows, d, d_rot, interleaved;
+    int32_t n_tensors, d, d_rot, interleaved;
     uint32_t n_tokens;
+    uint32_t tokens_of;    // tokens of a block (forward)
+    uint32_t table_tokens; // tokens that half of the table of angles holds (gradient), at least 2
     const int64_t *pos, *slots;
     int64_t pos0, n_slots;
     const uint64_t *step;  // [d_rot / 2] turns per position, as 64-bit fractions
-    float factor, sign, eps;
+    float factor, sign, eps, inv_d;
     float *partial;        // [grid][2][kMaxD] weight-gradient sums
 };
 
@@ -59,19 +66,60 @@ template <typename T> struct Num;
 template <> struct Num<__nv_bfloat16> {
     static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
     static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+    static __device__ __forceinline__ void get2(uint32_t w, float &a, float &b) {
+        a = __uint_as_float(w << 16);
+        b = __uint_as_float(w & 0xffff0000u);
+    }
+    static __device__ __forceinline__ uint32_t put2(float a, float b) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
 };
 template <> struct Num<__half> {
     static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
     static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
+    static __device__ __forceinline__ void get2(uint32_t w, float &a, float &b) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        a = v.x;
+        b = v.y;
+    }
+    static __device__ __forceinline__ uint32_t put2(float a, float b) {
+        const __half2 v = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
 };
 template <> struct Num<float> {
     static __device__ __forceinline__ float get(float v) { return v; }
     static __device__ __forceinline__ float put(float v) { return v; }
 };
 
-// VEC elements as they lie in memory
-template <typename T, int VEC> struct alignas(sizeof(T) * VEC) Pack {
-    T v[VEC];
+// VEC elements as they lie in memory: 16 bytes, or one element
+template <typename T, int VEC> struct Pack {
+    uint4 v;
+    __device__ __forceinline__ void load(const T *p) { v = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<uint4 *>(p) = v; }
+    __device__ __forceinline__ void widen(float *e) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 2) Num<T>::get2(w[i], e[2 * i], e[2 * i + 1]);
+            else e[i] = __uint_as_float(w[i]);
+        }
+    }
+    __device__ __forceinline__ void narrow(const float *e) {
+        if constexpr (sizeof(T) == 2)
+            v = make_uint4(Num<T>::put2(e[0], e[1]), Num<T>::put2(e[2], e[3]), Num<T>::put2(e[4], e[5]),
+                           Num<T>::put2(e[6], e[7]));
+        else
+            v = make_uint4(__float_as_uint(e[0]), __float_as_uint(e[1]), __float_as_uint(e[2]), __float_as_uint(e[3]));
+    }
+};
+template <typename T> struct Pack<T, 1> {
+    T v;
+    __device__ __forceinline__ void load(const T *p) { v = *p; }
+    __device__ __forceinline__ void store(T *p) const { *p = v; }
+    __device__ __forceinline__ void widen(float *e) const { *e = Num<T>::get(v); }
+    __device__ __forceinline__ void narrow(const float *e) { v = Num<T>::put(*e); }
 };
 
 // Where a lane's slots lie in a row.  Slot s of the rotated part holds VEC
@@ -103,56 +151,107 @@ template <int VEC, int L, int NS> struct Slots {
 };
 
 template <typename T, int VEC, int L, int NS>
-__device__ __forceinline__ void load_row(Pack<T, VEC> (&raw)[NS][2], const T *row, const Slots<VEC, L, NS> &s) {
-#pragma unroll
-    for (int n = 0; n < NS; ++n) {
-        if (s.has0[n]) raw[n][0] = *reinterpret_cast<const Pack<T, VEC> *>(row + s.o0[n]);
-        if (s.has1[n]) raw[n][1] = *reinterpret_cast<const Pack<T, VEC> *>(row + s.o1[n]);
-    }
-}
-
-template <typename T, int VEC, int L, int NS>
-__device__ __forceinline__ void widen(float (&e)[NS][2 * VEC], const Pack<T, VEC> (&raw)[NS][2],
-                                      const Slots<VEC, L, NS> &s) {
-#pragma unroll
-    for (int n = 0; n < NS; ++n)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            e[n][i] = s.has0[n] ? Num<T>::get(raw[n][0].v[i]) : 0.f;
-            e[n][VEC + i] = s.has1[n] ? Num<T>::get(raw[n][1].v[i]) : 0.f;
-        }
-}
-
-template <typename T, int VEC, int L, int NS>
 __device__ __forceinline__ void store_row(T *row, const float (&e)[NS][2 * VEC], const Slots<VEC, L, NS> &s) {
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
         Pack<T, VEC> a, b;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            a.v[i] = Num<T>::put(e[n][i]);
-            b.v[i] = Num<T>::put(e[n][VEC + i]);
-        }
-        if (s.has0[n]) *reinterpret_cast<Pack<T, VEC> *>(row + s.o0[n]) = a;
-        if (s.has1[n]) *reinterpret_cast<Pack<T, VEC> *>(row + s.o1[n]) = b;
+        a.narrow(e[n]);
+        b.narrow(e[n] + VEC);
+        if (s.has0[n]) a.store(row + s.o0[n]);
+        if (s.has1[n]) b.store(row + s.o1[n]);
     }
 }
 
-// (cos, sin) of the unit's position for the lane's pairs, times the factor
+// Two fp32 operations in one instruction (f32x2) on neighbouring elements
+using window::add2;
+using window::f2;
+using window::fma2;
+using window::mul2;
+using window::unf2;
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+template <int N> __device__ __forceinline__ uint64_t at2(const float (&e)[N], int i) { return f2(e[i], e[i + 1]); }
+
+// 16 bytes (or one element) of global memory into this thread's own slot of
+// shared memory, asynchronously
+template <typename T, int VEC> __device__ __forceinline__ void stage(Pack<T, VEC> *dst, const T *src) {
+    if constexpr (VEC == 1) {
+        dst->load(src);
+    } else {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+    }
+}
+__device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// A lane's slots of a row: staged as [slot][2][thread] packs, then widened
+template <typename T, int VEC, int L, int NS>
+__device__ __forceinline__ void stage_row(Pack<T, VEC> *st, const T *row, const Slots<VEC, L, NS> &s) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        if (s.has0[n]) stage(st + (2 * n) * kThreads + threadIdx.x, row + s.o0[n]);
+        if (s.has1[n]) stage(st + (2 * n + 1) * kThreads + threadIdx.x, row + s.o1[n]);
+    }
+}
+
+template <typename T, int VEC, int L, int NS>
+__device__ __forceinline__ void widen(float (&e)[NS][2 * VEC], const Pack<T, VEC> *st, const Slots<VEC, L, NS> &s) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        st[(2 * n) * kThreads + threadIdx.x].widen(e[n]);
+        st[(2 * n + 1) * kThreads + threadIdx.x].widen(e[n] + VEC);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            if (!s.has0[n]) e[n][i] = 0.f;
+            if (!s.has1[n]) e[n][VEC + i] = 0.f;
+        }
+    }
+}
+
+// r / heads for r < 2^31 (Tensor::magic, shift)
+__device__ __forceinline__ uint32_t divide(uint32_t r, uint32_t magic, uint32_t shift) {
+    return (uint32_t)(((uint64_t)r * magic) >> shift);
+}
+
+// The cosines and sines of tokens tok0 .. tok0 + n - 1, times the factor, by the
+// whole block: table[token][2][d_rot / 2].
+__device__ __forceinline__ void fill_table(float *table, const Args &a, uint32_t tok0, uint32_t n) {
+    const uint32_t half = (uint32_t)a.d_rot / 2;
+    for (uint32_t i = threadIdx.x; i < n * half; i += kThreads) {
+        const uint32_t t = i / half, f = i - t * half;
+        const int64_t pos = a.pos != nullptr ? a.pos[tok0 + t] : a.pos0 + (int64_t)(tok0 + t);
+        const uint64_t turn = (uint64_t)pos * a.step[f];
+        const float half_turns = (float)(int32_t)(uint32_t)(turn >> 32) * 4.656612873077393e-10f;  // 2^-31
+        float c, s;
+        sincospif(half_turns, &s, &c);
+        table[2 * t * half + f] = c * a.factor;
+        table[(2 * t + 1) * half + f] = s * a.factor * a.sign;
+    }
+}
+
+// The lane's part of a token's table
 template <int VEC, int L, int NS>
-__device__ __forceinline__ void angles(float (&cs)[NS][VEC], float (&sn)[NS][VEC], const Args &a, int64_t pos,
-                                       const Slots<VEC, L, NS> &s) {
+__device__ __forceinline__ void read_table(float (&cs)[NS][VEC], float (&sn)[NS][VEC], const float *table, const Args &a,
+                                           uint32_t t, const Slots<VEC, L, NS> &s) {
+    const float *c = table + 2 * t * (uint32_t)(a.d_rot / 2), *n = c + a.d_rot / 2;
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
-        if (s.rot[n]) {
+    for (int k = 0; k < NS; ++k)
+        if (s.rot[k]) {
+            if (VEC % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const uint64_t turn = (uint64_t)pos * a.step[s.f0[n] + i];
-                const float half_turns = (float)(int32_t)(uint32_t)(turn >> 32) * 4.656612873077393e-10f;  // 2^-31
-                float c, si;
-                sincospif(half_turns, &si, &c);
-                cs[n][i] = c * a.factor;
-                sn[n][i] = si * a.factor * a.sign;
+                for (int i = 0; i < VEC; i += 4) {
+                    *reinterpret_cast<float4 *>(&cs[k][i]) = *reinterpret_cast<const float4 *>(c + s.f0[k] + i);
+                    *reinterpret_cast<float4 *>(&sn[k][i]) = *reinterpret_cast<const float4 *>(n + s.f0[k] + i);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    cs[k][i] = c[s.f0[k] + i];
+                    sn[k][i] = n[s.f0[k] + i];
+                }
             }
         }
 }
@@ -170,13 +269,17 @@ __device__ __forceinline__ void turn(float (&e)[NS][2 * VEC], const float (&cs)[
                 e[n][2 * i] = u * cs[n][i] - v * sn[n][i];
                 e[n][2 * i + 1] = u * sn[n][i] + v * cs[n][i];
             }
-        } else {
+        } else if constexpr (VEC > 1) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float u = e[n][i], v = e[n][VEC + i];
-                e[n][i] = u * cs[n][i] - v * sn[n][i];
-                e[n][VEC + i] = u * sn[n][i] + v * cs[n][i];
+            for (int i = 0; i < VEC; i += 2) {
+                const uint64_t u = at2(e[n], i), v = at2(e[n], VEC + i), c = at2(cs[n], i), z = at2(sn[n], i);
+                unf2(sub2(mul2(u, c), mul2(v, z)), e[n][i], e[n][i + 1]);
+                unf2(fma2(u, z, mul2(v, c)), e[n][VEC + i], e[n][VEC + i + 1]);
             }
+        } else {
+            const float u = e[n][0], v = e[n][1];
+            e[n][0] = u * cs[n][0] - v * sn[n][0];
+            e[n][1] = u * sn[n][0] + v * cs[n][0];
         }
     }
 }
@@ -189,69 +292,105 @@ template <int L> __device__ __forceinline__ float group_sum(float v, uint32_t ma
 }
 
 template <typename T, int VEC, int L, int NS>
-__device__ __forceinline__ void load_weight(float (&w)[NS][2 * VEC], const Tensor &x, const Slots<VEC, L, NS> &s) {
+__device__ __forceinline__ void load_weight(float (&w)[NS][2 * VEC], const void *weight, const Slots<VEC, L, NS> &s) {
+    const T *p = static_cast<const T *>(weight);
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+#pragma unroll
+        for (int i = 0; i < 2 * VEC; ++i) w[n][i] = 1.f;
+        Pack<T, VEC> a;
+        if (p != nullptr && s.has0[n]) {
+            a.load(p + s.o0[n]);
+            a.widen(w[n]);
+        }
+        if (p != nullptr && s.has1[n]) {
+            a.load(p + s.o1[n]);
+            a.widen(w[n] + VEC);
+        }
+    }
+}
+
+// sum of squares of the lane's elements (an even number)
+template <int NS, int E> __device__ __forceinline__ float squares(const float (&e)[NS][E]) {
+    uint64_t q = f2(0.f, 0.f);
 #pragma unroll
     for (int n = 0; n < NS; ++n)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            w[n][i] = x.w != nullptr && s.has0[n] ? Num<T>::get(static_cast<const T *>(x.w)[s.o0[n] + i]) : 1.f;
-            w[n][VEC + i] = x.w != nullptr && s.has1[n] ? Num<T>::get(static_cast<const T *>(x.w)[s.o1[n] + i]) : 1.f;
-        }
+        for (int i = 0; i < E; i += 2) q = fma2(at2(e[n], i), at2(e[n], i), q);
+    float a, b;
+    unf2(q, a, b);
+    return a + b;
 }
 
-// The forward of both operators (and, with sign -1, the gradient of the rotation).
-template <typename T, int VEC, int L, int NS, bool NORM>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Args a) {
-    constexpr int U = VEC == 1 ? 1 : 2;  // rows whose loads are in flight together
+// Shared memory for the gradient's staged rows, or its sums where they are more
+template <typename T, int VEC, int NS, int U> __host__ __device__ constexpr int grad_stage_bytes() {
+    const int rows = 2 * U * 2 * 2 * NS * kThreads * (int)sizeof(Pack<T, VEC>), sums = kThreads * NS * 2 * VEC * 4;
+    return ((rows > sums ? rows : sums) + 15) / 16 * 16;
+}
+
+// The forward of both operators (and, with sign -1, the gradient of the
+// rotation): a block takes a.tokens_of tokens.  U: rows of a group that are
+// under way together, each lane's in its own slots of shared memory, so that
+// they cost no registers.
+template <typename T, int VEC, int L, int NS, int U, bool NORM>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) rope_kernel(const __grid_constant__ Args a) {
+    constexpr int G = kThreads / L;
+    __shared__ Pack<T, VEC> staged[U][2 * NS * kThreads];
+    extern __shared__ __align__(16) float table[];
     const int sub = (int)threadIdx.x % L;
+    const uint32_t grp = threadIdx.x / L;
     const uint32_t mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << ((threadIdx.x & 31u) & ~(uint32_t)(L - 1));
-    uint32_t total = 0;
-    for (int x = 0; x < a.n_tensors; ++x) total += a.n_tokens * (uint32_t)a.t[x].splits;
-    const uint32_t groups = gridDim.x * (kThreads / L);
-    for (uint32_t u = blockIdx.x * (kThreads / L) + threadIdx.x / L; u < total; u += groups) {
-        uint32_t v = u;
-        int x = 0;
-        while (v >= a.n_tokens * (uint32_t)a.t[x].splits) v -= a.n_tokens * (uint32_t)a.t[x++].splits;
+    const uint32_t tok0 = blockIdx.x * a.tokens_of, n_tok = min(a.tokens_of, a.n_tokens - tok0);
+    bool filled = false;
+    for (int x = 0; x < a.n_tensors; ++x) {
         const Tensor &t = a.t[x];
-        const uint32_t tok = v / (uint32_t)t.splits;
-        const int h0 = (int)(v - tok * (uint32_t)t.splits) * a.rows;
-        const int h1 = min(h0 + a.rows, t.heads);
-        int64_t to = tok;
-        if (t.scatter) {
-            to = a.slots[tok];
-            if (to < 0 || to >= a.n_slots) continue;
-        }
+        const bool copy = t.copy, norm = NORM && t.norm, scatter = t.scatter;
+        const uint32_t heads = (uint32_t)t.heads, magic = t.magic, shift = t.shift, rows = n_tok * heads;
+        const T *src = static_cast<const T *>(t.x) + (int64_t)tok0 * t.xt;
+        T *dst = static_cast<T *>(t.y);
+        const int64_t xt = t.xt, xh = t.xh, yt = t.yt, yh = t.yh;
         Slots<VEC, L, NS> s;
-        s.init(a, t.copy != 0, sub);
-        float cs[NS][VEC], sn[NS][VEC], w[NS][2 * VEC];
-        angles(cs, sn, a, a.pos != nullptr ? a.pos[tok] : a.pos0 + (int64_t)tok, s);
-        if (NORM && t.norm) load_weight<T>(w, t, s);
-        const T *src = static_cast<const T *>(t.x) + (int64_t)tok * t.xt;
-        T *dst = static_cast<T *>(t.y) + to * t.yt;
-        for (int h = h0; h < h1; h += U) {
-            Pack<T, VEC> raw[U][NS][2];
+        s.init(a, copy, sub);
+        float w[NS][2 * VEC];
+        if (norm) load_weight<T>(w, t.w, s);
+        for (uint32_t r0 = grp; r0 - grp < rows; r0 += G * U) {
+            uint32_t tok[U];
 #pragma unroll
-            for (int r = 0; r < U; ++r)
-                if (h + r < h1) load_row(raw[r], src + (h + r) * t.xh, s);
+            for (int u = 0; u < U; ++u) {
+                const uint32_t r = r0 + u * G;
+                tok[u] = divide(r, magic, shift);
+                if (r < rows) stage_row(staged[u], src + (int64_t)tok[u] * xt + (int64_t)(r - tok[u] * heads) * xh, s);
+            }
+            stage_commit();
+            if (!filled) {
+                fill_table(table, a, tok0, n_tok);
+                __syncthreads();
+                filled = true;
+            }
+            stage_wait<0>();
 #pragma unroll
-            for (int r = 0; r < U; ++r) {
-                if (h + r >= h1) break;
-                float e[NS][2 * VEC];
-                widen(e, raw[r], s);
-                if (NORM && t.norm) {
-                    float q = 0.f;
-#pragma unroll
-                    for (int n = 0; n < NS; ++n)
-#pragma unroll
-                        for (int i = 0; i < 2 * VEC; ++i) q = fmaf(e[n][i], e[n][i], q);
-                    const float inv = rsqrtf(group_sum<L>(q, mask) / (float)a.d + a.eps);
-#pragma unroll
-                    for (int n = 0; n < NS; ++n)
-#pragma unroll
-                        for (int i = 0; i < 2 * VEC; ++i) e[n][i] *= inv * w[n][i];
+            for (int u = 0; u < U; ++u) {
+                const uint32_t r = r0 + u * G;
+                if (r >= rows) break;
+                int64_t to = (int64_t)tok0 + tok[u];
+                if (scatter) {
+                    to = a.slots[to];
+                    if (to < 0 || to >= a.n_slots) continue;
                 }
+                float e[NS][2 * VEC];
+                widen(e, staged[u], s);
+                if (norm) {
+                    const float inv = rsqrtf(group_sum<L>(squares(e), mask) * a.inv_d + a.eps);
+#pragma unroll
+                    for (int n = 0; n < NS; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2 * VEC; i += 2)
+                            unf2(mul2(mul2(at2(e[n], i), f2(inv, inv)), at2(w[n], i)), e[n][i], e[n][i + 1]);
+                }
+                float cs[NS][VEC], sn[NS][VEC];
+                read_table(cs, sn, table, a, tok[u], s);
                 turn(e, cs, sn, a, s);
-                store_row(dst + (h + r) * t.yh, e, s);
+                store_row(dst + to * yt + (int64_t)(r - tok[u] * heads) * yh, e, s);
             }
         }
     }
@@ -260,64 +399,102 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 // The gradient of norm and rotation.  With g = R^T dy, r = rsqrt(mean x^2 + eps):
 // dx = r (g w - x r mean(g w x r)), dw = sum over rows of g x r.  A lane sums
 // its elements' dw over all its rows in registers, a block its groups' sums in
-// shared memory, and norm_dw_kernel the blocks' -- each in a fixed order.
-template <typename T, int VEC, int L, int NS>
-__global__ void __launch_bounds__(kThreads) norm_grad_kernel(const __grid_constant__ Args a) {
+// shared memory, and norm_dw_kernel the blocks' -- each in a fixed order.  The
+// blocks are persistent, so that there are few partial sums, and each step's
+// rows are staged while the step before is computed.
+template <typename T, int VEC, int L, int NS, int U>
+__global__ void __launch_bounds__(kThreads, kGradBlocksPerSm) norm_grad_kernel(const __grid_constant__ Args a) {
     constexpr int G = kThreads / L;
-    __shared__ float sums[kThreads * NS * 2 * VEC];  // [group][element]
-    const int sub = (int)threadIdx.x % L, grp = (int)threadIdx.x / L;
+    constexpr int kSlots = 2 * NS * kThreads;
+    extern __shared__ __align__(16) uint8_t sm[];
+    Pack<T, VEC> *staged = reinterpret_cast<Pack<T, VEC> *>(sm);               // [2][U][x, dy][slots]
+    float *sums = reinterpret_cast<float *>(sm);                               // [group][element], at the end
+    float *table = reinterpret_cast<float *>(sm + grad_stage_bytes<T, VEC, NS, U>());  // [2][token][2][d_rot / 2]
+    const int sub = (int)threadIdx.x % L;
+    const uint32_t grp = threadIdx.x / L;
     const uint32_t mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << ((threadIdx.x & 31u) & ~(uint32_t)(L - 1));
-    const uint32_t groups = gridDim.x * G;
     Slots<VEC, L, NS> s;
     s.init(a, false, sub);
     for (int x = 0; x < a.n_tensors; ++x) {
         const Tensor &t = a.t[x];
+        const uint32_t heads = (uint32_t)t.heads, magic = t.magic, shift = t.shift;
+        // a step: up to G * U consecutive rows of the tensor whose tokens' angles fit the table
+        const uint32_t rows = a.n_tokens * heads, per = min((uint32_t)(G * U), (a.table_tokens - 1) * heads);
+        const int64_t xt = t.xt, xh = t.xh, gt = t.gt, gh = t.gh, yt = t.yt, yh = t.yh;
+        const T *src = static_cast<const T *>(t.x), *grd = static_cast<const T *>(t.dy);
+        T *dst = static_cast<T *>(t.y);
         float w[NS][2 * VEC], acc[NS][2 * VEC];
-        load_weight<T>(w, t, s);
+        load_weight<T>(w, t.w, s);
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int i = 0; i < 2 * VEC; ++i) acc[n][i] = 0.f;
-        const uint32_t units = a.n_tokens * (uint32_t)t.splits;
-        for (uint32_t u = blockIdx.x * G + grp; u < units; u += groups) {
-            const uint32_t tok = u / (uint32_t)t.splits;
-            const int h0 = (int)(u - tok * (uint32_t)t.splits) * a.rows;
-            const int h1 = min(h0 + a.rows, t.heads);
-            float cs[NS][VEC], sn[NS][VEC];
-            angles(cs, sn, a, a.pos != nullptr ? a.pos[tok] : a.pos0 + (int64_t)tok, s);
-            const T *src = static_cast<const T *>(t.x) + (int64_t)tok * t.xt;
-            const T *grd = static_cast<const T *>(t.dy) + (int64_t)tok * t.gt;
-            T *dst = static_cast<T *>(t.y) + (int64_t)tok * t.yt;
-            for (int h = h0; h < h1; ++h) {
-                Pack<T, VEC> rx[NS][2], rg[NS][2];
-                load_row(rx, src + h * t.xh, s);
-                load_row(rg, grd + h * t.gh, s);
+        auto issue = [&](uint32_t r0, uint32_t half) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t r = r0 + (uint32_t)(u * G) + grp;
+                if ((uint32_t)(u * G) + grp < per && r < rows) {
+                    const uint32_t tok = divide(r, magic, shift);
+                    const int64_t h = (int64_t)(r - tok * heads);
+                    Pack<T, VEC> *st = staged + (half * U + u) * 2 * kSlots;
+                    stage_row(st, src + (int64_t)tok * xt + h * xh, s);
+                    stage_row(st + kSlots, grd + (int64_t)tok * gt + h * gh, s);
+                }
+            }
+            stage_commit();
+        };
+        const uint32_t step = gridDim.x * per;
+        uint32_t half = 0;
+        issue(blockIdx.x * per, half);
+        for (uint32_t r0 = blockIdx.x * per; r0 < rows; r0 += step, half ^= 1u) {
+            const uint32_t r1 = min(r0 + per, rows), tok0 = divide(r0, magic, shift);
+            issue(r0 + step < rows ? r0 + step : rows, half ^ 1u);
+            float *tab = table + half * a.table_tokens * (uint32_t)a.d_rot;
+            fill_table(tab, a, tok0, divide(r1 - 1, magic, shift) - tok0 + 1);
+            __syncthreads();
+            stage_wait<1>();
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t r = r0 + (uint32_t)(u * G) + grp;
+                if (r >= r1) break;
+                const uint32_t tok = divide(r, magic, shift);
+                const Pack<T, VEC> *st = staged + (half * U + u) * 2 * kSlots;
                 float e[NS][2 * VEC], g[NS][2 * VEC];
-                widen(e, rx, s);
-                widen(g, rg, s);
-                turn(g, cs, sn, a, s);
-                float q = 0.f, m = 0.f;  // sums of x^2 and of g w x
+                {
+                    float cs[NS][VEC], sn[NS][VEC];
+                    widen(g, st + kSlots, s);
+                    read_table(cs, sn, tab, a, tok - tok0, s);
+                    turn(g, cs, sn, a, s);
+                }
+                widen(e, st, s);
+                float gw[NS][2 * VEC];
+                uint64_t m2 = f2(0.f, 0.f);  // sums of g w x
 #pragma unroll
                 for (int n = 0; n < NS; ++n)
 #pragma unroll
-                    for (int i = 0; i < 2 * VEC; ++i) {
-                        q = fmaf(e[n][i], e[n][i], q);
-                        m = fmaf(g[n][i] * w[n][i], e[n][i], m);
+                    for (int i = 0; i < 2 * VEC; i += 2) {
+                        const uint64_t v = mul2(at2(g[n], i), at2(w[n], i));
+                        unf2(v, gw[n][i], gw[n][i + 1]);
+                        m2 = fma2(v, at2(e[n], i), m2);
                     }
-                const float inv = rsqrtf(group_sum<L>(q, mask) / (float)a.d + a.eps);
-                const float mean = group_sum<L>(m, mask) * inv / (float)a.d;
+                float m0, m1;
+                unf2(m2, m0, m1);
+                const float inv = rsqrtf(group_sum<L>(squares(e), mask) * a.inv_d + a.eps);
+                const float mean = group_sum<L>(m0 + m1, mask) * inv * a.inv_d;
+                const uint64_t inv2 = f2(inv, inv), k2 = f2(-inv * mean, -inv * mean);
 #pragma unroll
                 for (int n = 0; n < NS; ++n)
 #pragma unroll
-                    for (int i = 0; i < 2 * VEC; ++i) {
-                        const float xh = e[n][i] * inv;
-                        acc[n][i] = fmaf(g[n][i], xh, acc[n][i]);
-                        e[n][i] = inv * (g[n][i] * w[n][i] - xh * mean);
+                    for (int i = 0; i < 2 * VEC; i += 2) {
+                        const uint64_t h = mul2(at2(e[n], i), inv2);
+                        unf2(fma2(at2(g[n], i), h, at2(acc[n], i)), acc[n][i], acc[n][i + 1]);
+                        unf2(fma2(h, k2, mul2(at2(gw[n], i), inv2)), e[n][i], e[n][i + 1]);
                     }
-                store_row(dst + h * t.yh, e, s);
+                store_row(dst + (int64_t)tok * yt + (int64_t)(r - tok * heads) * yh, e, s);
             }
         }
-        __syncthreads();  // the previous tensor's sums have been read
+        stage_wait<0>();
+        __syncthreads();  // every lane has read its staged rows
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -331,6 +508,7 @@ __global__ void __launch_bounds__(kThreads) norm_grad_kernel(const __grid_consta
             for (int k = 0; k < G; ++k) v += sums[k * a.d + j];
             a.partial[((int64_t)blockIdx.x * 2 + x) * kMaxD + j] = v;
         }
+        __syncthreads();  // the sums have been read
     }
 }
 
@@ -426,33 +604,49 @@ int check_rows(const char *name, const void *p, int size, int heads, bool any) {
     return SYN_OK;
 }
 
-// Units of up to a.rows heads of one token: few heads while that is what fills
-// the SMs (the angles are computed again for each unit), up to kRows after.
-void split_rows(Args &a, int num_sms, int lanes) {
-    int64_t rows = 0;
-    for (int x = 0; x < a.n_tensors; ++x) rows += (int64_t)a.n_tokens * a.t[x].heads;
-    const int64_t fill = (int64_t)num_sms * 1024 / lanes;
-    a.rows = (int32_t)std::min<int64_t>(kRows, std::max<int64_t>(1, rows / fill));
-    for (int x = 0; x < a.n_tensors; ++x) a.t[x].splits = (a.t[x].heads + a.rows - 1) / a.rows;
-}
-
-int64_t units_of(const Args &a) {
-    int64_t n = 0;
-    for (int x = 0; x < a.n_tensors; ++x) n += (int64_t)a.n_tokens * a.t[x].splits;
-    return n;
-}
-
 enum Kind { kTurn, kNorm, kNormGrad };
 
-template <typename T, int VEC, int L, int NS> int launch(syn_rope_plan_s *pl, Args &a, Kind kind, cudaStream_t st, int &grid) {
-    split_rows(a, pl->num_sms, L);
-    const int64_t units = units_of(a);
-    grid = (int)std::min<int64_t>((units + kThreads / L - 1) / (kThreads / L), (int64_t)pl->num_sms * kBlocksPerSm);
-    if (kind == kTurn) rope_kernel<T, VEC, L, NS, false><<<grid, kThreads, 0, st>>>(a);
-    else if (kind == kNorm) rope_kernel<T, VEC, L, NS, true><<<grid, kThreads, 0, st>>>(a);
-    else norm_grad_kernel<T, VEC, L, NS><<<grid, kThreads, 0, st>>>(a);
+// Tokens whose rows of `heads` heads fill a block that walks `rows` rows, as
+// far as their angles (d_rot floats a token) fit `bytes`; at least one.
+uint32_t tokens_for(int64_t rows, int64_t heads, int d_rot, int bytes) {
+    return (uint32_t)std::max<int64_t>(1, std::min<int64_t>(rows / heads, bytes / (4 * std::max(d_rot, 1))));
+}
+
+template <typename T, int VEC, int L, int NS, int U, bool NORM> int launch_forward(Args &a, cudaStream_t st) {
+    int most = 1;
+    for (int x = 0; x < a.n_tensors; ++x) most = std::max(most, a.t[x].heads);
+    a.tokens_of = U > 1 ? tokens_for(kThreads / L * U, most, a.d_rot, kTableBytes) : 1;
+    const unsigned grid = (a.n_tokens + a.tokens_of - 1) / a.tokens_of;
+    rope_kernel<T, VEC, L, NS, U, NORM><<<grid, kThreads, (size_t)a.tokens_of * (size_t)a.d_rot * 4, st>>>(a);
     ROPE_CK(cudaGetLastError());
     return SYN_OK;
+}
+
+template <typename T, int VEC, int L, int NS> int launch(syn_rope_plan_s *pl, Args &a, Kind kind, cudaStream_t st, int &grid) {
+    constexpr int G = kThreads / L, kMany = VEC == 1 ? 1 : kRowsPerLane;
+    if (kind == kNormGrad) {
+        constexpr int U = VEC == 1 ? 1 : kRowsPerLane / 2;
+        a.table_tokens = 1;
+        int64_t blocks = 1;
+        for (int x = 0; x < a.n_tensors; ++x) {
+            const int64_t heads = a.t[x].heads, most = kTableBytes / (4 * std::max(a.d_rot, 1));
+            a.table_tokens = std::max<uint32_t>(a.table_tokens, (uint32_t)std::min<int64_t>(most, (G * U - 1) / heads + 2));
+            blocks = std::max<int64_t>(blocks, ((int64_t)a.n_tokens * heads + G * U - 1) / (G * U));
+        }
+        grid = (int)std::min<int64_t>(blocks, (int64_t)pl->num_sms * kGradBlocksPerSm);
+        const size_t smem = (size_t)grad_stage_bytes<T, VEC, NS, U>() + (size_t)a.table_tokens * (size_t)a.d_rot * 8;
+        ROPE_CK(cudaFuncSetAttribute(norm_grad_kernel<T, VEC, L, NS, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        norm_grad_kernel<T, VEC, L, NS, U><<<grid, kThreads, smem, st>>>(a);
+        ROPE_CK(cudaGetLastError());
+        return SYN_OK;
+    }
+    // several rows a lane once that still leaves every SM a few blocks
+    int64_t rows = 0;
+    for (int x = 0; x < a.n_tensors; ++x) rows += (int64_t)a.n_tokens * a.t[x].heads;
+    const bool many = rows >= (int64_t)pl->num_sms * 4 * G * kMany;
+    if (kind == kTurn)
+        return many ? launch_forward<T, VEC, L, NS, kMany, false>(a, st) : launch_forward<T, VEC, L, NS, 1, false>(a, st);
+    return many ? launch_forward<T, VEC, L, NS, kMany, true>(a, st) : launch_forward<T, VEC, L, NS, 1, true>(a, st);
 }
 
 // A lane's slot is two 16-byte vectors where every row, stride and both parts
@@ -475,17 +669,25 @@ int run(syn_rope_plan_s *pl, Args &a, Kind kind, cudaStream_t st, int &grid) {
     a.interleaved = c.layout == SYN_ROPE_INTERLEAVED;
     a.step = pl->d_step;
     a.factor = (float)pl->factor;
+    a.inv_d = 1.f / (float)c.d;
     a.partial = pl->d_partial;
     const int size = elem_size(c.dtype);
     bool vec = c.d % (32 / size) == 0 && c.d_rot % (32 / size) == 0;
     int64_t rows = 0;
     for (int x = 0; x < a.n_tensors; ++x) {
         const Tensor &t = a.t[x];
-        vec = vec && vector_rows(t.x, t.xt, t.xh, size) && vector_rows(t.y, t.yt, t.yh, size) &&
+        vec = vec && vector_rows(t.w, 0, 0, size) && vector_rows(t.x, t.xt, t.xh, size) && vector_rows(t.y, t.yt, t.yh, size) &&
               (t.dy == nullptr || vector_rows(t.dy, t.gt, t.gh, size));
         rows += (int64_t)a.n_tokens * t.heads;
     }
     if (rows == 0) return SYN_OK;
+    for (int x = 0; x < a.n_tensors; ++x) {  // rows stay below 2^31
+        Tensor &t = a.t[x];
+        uint32_t bits = 0;
+        while (((int64_t)1 << bits) < t.heads) ++bits;
+        t.shift = 31 + bits;
+        t.magic = (uint32_t)((((uint64_t)1 << t.shift) + (uint64_t)t.heads - 1) / (uint64_t)t.heads);
+    }
     if (rows >= (int64_t)1 << 31) return host_fail(SYN_ERR_UNSUPPORTED, "2^31 or more rows in one call");
     if (c.dtype == SYN_DTYPE_BF16) return dispatch<__nv_bfloat16>(pl, a, kind, vec, st, grid);
     if (c.dtype == SYN_DTYPE_F16) return dispatch<__half>(pl, a, kind, vec, st, grid);
@@ -601,7 +803,7 @@ int syn_rope_plan_create(syn_rope_plan_t *out, const syn_rope_cfg_t *cfg) {
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&pl->num_sms, cudaDevAttrMultiProcessorCount, pl->device);
     if (e == cudaSuccess) e = cudaMalloc(&pl->d_step, std::max<size_t>(step.size(), 1) * sizeof(uint64_t));
     if (e == cudaSuccess)
-        e = cudaMalloc(&pl->d_partial, (size_t)pl->num_sms * kBlocksPerSm * 2 * kMaxD * sizeof(float));
+        e = cudaMalloc(&pl->d_partial, (size_t)pl->num_sms * kGradBlocksPerSm * 2 * kMaxD * sizeof(float));
     if (e == cudaSuccess && !step.empty())
         e = cudaMemcpy(pl->d_step, step.data(), step.size() * sizeof(uint64_t), cudaMemcpyHostToDevice);
     if (e != cudaSuccess) {

@@ -8,6 +8,7 @@ from __future__ import annotations
 import ctypes
 
 import numpy as np
+from torch import float32 as _float32, int64 as _int64
 
 from . import syn
 
@@ -89,19 +90,23 @@ def torch_dtype(dtype):
     return {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}[dtype]
 
 
-def check_heads(name, t, dtype, d, tokens=None, heads=None):
-    """A CUDA tensor [tokens, heads, d] of the plan's type with contiguous heads."""
-    if t.dtype != dtype or not t.is_cuda:
+def heads_of(name, t, dtype, d, tokens, heads=None):
+    """(address, token stride, head stride, heads) of a CUDA tensor [tokens,
+    heads, d] of type `dtype` with contiguous heads; None: any number."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not dtype or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor of type {dtype}")
-    if t.dim() != 3 or t.shape[2] != d or (t.shape[2] > 1 and t.stride(2) != 1):
+    if len(shape) != 3 or shape[2] != d or (stride[2] != 1 and d > 1):
         raise ValueError(f"{name} must be [tokens, heads, {d}] with contiguous heads")
-    if (tokens is not None and t.shape[0] != tokens) or (heads is not None and t.shape[1] != heads):
+    if (tokens is not None and shape[0] != tokens) or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must have {tokens} rows of {heads} heads")
+    return t.data_ptr(), stride[0], stride[1], shape[1]
 
 
 def check_vector(name, t, dtype, n):
-    if t.dtype != dtype or not t.is_cuda or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_cuda or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} {dtype}")
+    return t.data_ptr()
 
 
 class RopePlan:
@@ -111,7 +116,7 @@ class RopePlan:
         self._L = lib()
         self._h = _P()
         self.cfg = make_cfg(**cfg)
-        self.dtype = torch_dtype(cfg.get("dtype", "bf16"))
+        self.dtype, self._d = torch_dtype(cfg.get("dtype", "bf16")), self.cfg.d
         _check(self._L.syn_rope_plan_create(ctypes.byref(self._h), ctypes.byref(self.cfg)), "syn_rope_plan_create")
 
     def close(self):
@@ -140,35 +145,30 @@ class RopePlan:
     def _rows(self, name, x, y, tokens, slots=False):
         if x is None:
             return None
-        check_heads(name, x, self.dtype, self.cfg.d, tokens)
-        check_heads(name + "_out", y, self.dtype, self.cfg.d, None if slots else tokens, x.shape[1])
-        return ctypes.byref(Rows(syn._ptr(x), x.stride(0), x.stride(1), syn._ptr(y), y.stride(0), y.stride(1), x.shape[1]))
-
-    def _index(self, name, t, n):
-        import torch
-        if t is not None:
-            check_vector(name, t, torch.int64, n)
-        return syn._ptr(t)
+        d, dtype = self._d, self.dtype
+        p, xt, xh, heads = heads_of(name, x, dtype, d, tokens)
+        q, yt, yh, _ = heads_of(name + "_out", y, dtype, d, None if slots else tokens, heads)
+        return Rows(p, xt, xh, q, yt, yh, heads)
 
     def _forward(self, q, q_out, wq, k, k_out, wk, eps, v, v_out, positions, pos0, slots, stream, norm):
-        first = next((t for t in (q, k, v) if t is not None), None)
+        first = q if q is not None else k if k is not None else v
         if first is None:
             raise ValueError("one of q, k and v is needed")
-        n = first.shape[0]
-        rows = [self._rows("q", q, q_out, n), self._rows("k", k, k_out, n, slots is not None),
-                self._rows("v", v, v_out, n, slots is not None)]
-        pos, slot = self._index("positions", positions, n), self._index("slots", slots, n)
-        outs = [o.shape[0] for t, o in ((k, k_out), (v, v_out)) if t is not None]
-        n_slots = min(outs) if slots is not None and outs else 0
-        st = syn._stream(stream)
+        n, scatter, n_slots = first.shape[0], slots is not None, 0
+        rq = self._rows("q", q, q_out, n)
+        rk, rv = self._rows("k", k, k_out, n, scatter), self._rows("v", v, v_out, n, scatter)
+        pos = None if positions is None else check_vector("positions", positions, _int64, n)
+        slot = None
+        if scatter:
+            slot = check_vector("slots", slots, _int64, n)
+            n_slots = min((o.shape[0] for t, o in ((k, k_out), (v, v_out)) if t is not None), default=0)
         if not norm:
-            _check(self._L.syn_rope(self._h, *rows, pos, pos0, slot, n_slots, n, st), "syn_rope")
+            _check(self._L.syn_rope(self._h, rq, rk, rv, pos, pos0, slot, n_slots, n, syn._stream(stream)), "syn_rope")
             return
-        for name, w in (("wq", wq), ("wk", wk)):
-            if w is not None:
-                check_vector(name, w, self.dtype, self.cfg.d)
-        _check(self._L.syn_qk_norm_rope(self._h, rows[0], syn._ptr(wq), rows[1], syn._ptr(wk), eps, rows[2], pos, pos0,
-                                        slot, n_slots, n, st), "syn_qk_norm_rope")
+        a = None if wq is None else check_vector("wq", wq, self.dtype, self._d)
+        b = None if wk is None else check_vector("wk", wk, self.dtype, self._d)
+        _check(self._L.syn_qk_norm_rope(self._h, rq, a, rk, b, eps, rv, pos, pos0, slot, n_slots, n, syn._stream(stream)),
+               "syn_qk_norm_rope")
 
     def rotate(self, q, q_out, k=None, k_out=None, v=None, v_out=None, positions=None, pos0=0, slots=None, stream=None):
         """Rotate q and k, copy v; with `slots`, k and v go to those rows of k_out and v_out."""
@@ -185,23 +185,20 @@ class RopePlan:
         if first is None:
             raise ValueError("one of dq_out and dk_out is needed")
         n = first.shape[0]
+        pos = None if positions is None else check_vector("positions", positions, _int64, n)
         _check(self._L.syn_rope_backward(self._h, self._rows("dq_out", dq_out, dq, n), self._rows("dk_out", dk_out, dk, n),
-                                         self._index("positions", positions, n), pos0, n, syn._stream(stream)),
-               "syn_rope_backward")
+                                         pos, pos0, n, syn._stream(stream)), "syn_rope_backward")
 
     def _grad(self, name, x, dy, dx, w, dw, n):
-        import torch
         if x is None:
             return None
-        check_heads(name, x, self.dtype, self.cfg.d, n)
-        check_heads("d" + name + "_out", dy, self.dtype, self.cfg.d, n, x.shape[1])
-        check_heads("d" + name, dx, self.dtype, self.cfg.d, n, x.shape[1])
-        if w is not None:
-            check_vector("w" + name, w, self.dtype, self.cfg.d)
-        if dw is not None:
-            check_vector("dw" + name, dw, torch.float32, self.cfg.d)
-        return ctypes.byref(Grad(syn._ptr(x), x.stride(0), x.stride(1), syn._ptr(dy), dy.stride(0), dy.stride(1),
-                                 syn._ptr(dx), dx.stride(0), dx.stride(1), syn._ptr(w), syn._ptr(dw), x.shape[1]))
+        d, dtype = self._d, self.dtype
+        p, xt, xh, heads = heads_of(name, x, dtype, d, n)
+        g, gt, gh, _ = heads_of("d" + name + "_out", dy, dtype, d, n, heads)
+        o, ot, oh, _ = heads_of("d" + name, dx, dtype, d, n, heads)
+        a = None if w is None else check_vector("w" + name, w, dtype, d)
+        b = None if dw is None else check_vector("dw" + name, dw, _float32, d)
+        return Grad(p, xt, xh, g, gt, gh, o, ot, oh, a, b, heads)
 
     def norm_rotate_backward(self, q, dq_out, dq, wq, dwq, k=None, dk_out=None, dk=None, wk=None, dwk=None,
                              positions=None, pos0=0, eps=1e-6, stream=None):
@@ -211,7 +208,7 @@ class RopePlan:
         if first is None:
             raise ValueError("one of q and k is needed")
         n = first.shape[0]
+        pos = None if positions is None else check_vector("positions", positions, _int64, n)
         _check(self._L.syn_qk_norm_rope_backward(self._h, self._grad("q", q, dq_out, dq, wq, dwq, n),
-                                                 self._grad("k", k, dk_out, dk, wk, dwk, n), eps,
-                                                 self._index("positions", positions, n), pos0, n, syn._stream(stream)),
-               "syn_qk_norm_rope_backward")
+                                                 self._grad("k", k, dk_out, dk, wk, dwk, n), eps, pos, pos0, n,
+                                                 syn._stream(stream)), "syn_qk_norm_rope_backward")

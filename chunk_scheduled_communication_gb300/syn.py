@@ -203,9 +203,9 @@ def _ptr(t) -> int:
 
 
 def _stream(stream) -> int:
-    if stream is None:
+    if stream is None:  # the current device's current stream, without building a Stream object
         import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)

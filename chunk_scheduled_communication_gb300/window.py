@@ -8,9 +8,10 @@ from __future__ import annotations
 import ctypes
 
 import numpy as np
+from torch import float32 as _float32, int32 as _int32
 
 from . import syn
-from .rope import DTYPES, check_heads, check_vector, torch_dtype
+from .rope import DTYPES, check_vector, heads_of, torch_dtype
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -82,16 +83,15 @@ def _check(status, where):
 
 
 def _rows(name, t, dtype, d, rows, heads):
-    check_heads(name, t, dtype, d, rows, heads)
-    return Rows(syn._ptr(t), t.stride(0), t.stride(1))
+    return Rows(*heads_of(name, t, dtype, d, rows, heads)[:3])
 
 
 def _lse(lse, rows, heads):
-    import torch
-    if lse is not None and (lse.dtype != torch.float32 or not lse.is_cuda or tuple(lse.shape) != (rows, heads)
-                            or not lse.is_contiguous()):
+    if lse is None:
+        return None
+    if lse.dtype is not _float32 or not lse.is_cuda or lse.shape != (rows, heads) or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous CUDA tensor [{rows}, {heads}] of float32")
-    return syn._ptr(lse)
+    return lse.data_ptr()
 
 
 class WindowPlan:
@@ -179,7 +179,7 @@ class DecodePlan:
         _check(self._L.syn_decode_cfg_default(ctypes.byref(c)), "syn_decode_cfg_default")
         c.dtype, c.max_seqs, c.H_q, c.H_kv, c.d = DTYPES[dtype], max_seqs, H_q, H_kv, d
         c.window, c.sinks, c.page_size, c.scale = window, sinks, page_size, scale
-        self.cfg, self.dtype = c, torch_dtype(dtype)
+        self.cfg, self.dtype, self._page = c, torch_dtype(dtype), (page_size, H_kv, d)
         _check(self._L.syn_decode_plan_create(ctypes.byref(self._h), ctypes.byref(c)), "syn_decode_plan_create")
 
     def close(self):
@@ -200,33 +200,31 @@ class DecodePlan:
         self.close()
 
     def _cache(self, name, t):
-        c = self.cfg
-        if t.dtype != self.dtype or not t.is_cuda or t.dim() != 4 or tuple(t.shape[1:]) != (c.page_size, c.H_kv, c.d) \
-                or t.stride(3) != 1:
+        c, shape, stride = self.cfg, t.shape, t.stride()
+        if t.dtype is not self.dtype or not t.is_cuda or len(shape) != 4 or shape[1:] != self._page or stride[3] != 1:
             raise ValueError(f"{name} must be a CUDA tensor [pages, {c.page_size}, {c.H_kv}, {c.d}] of type {self.dtype} "
                              "with contiguous heads")
-        return Cache(syn._ptr(t), t.stride(0), t.stride(1), t.stride(2))
+        return Cache(t.data_ptr(), stride[0], stride[1], stride[2])
 
     def run(self, q, k_cache, v_cache, seq_lens, O, lse=None, page_table=None, stream=None):
         """O of each sequence's last token q[s] over its seq_lens[s] cached tokens.
         page_table: int32 [sequences, pages of a sequence]; None: sequence s is page s."""
-        import torch
         c, n = self.cfg, q.shape[0]
-        qr = _rows("q", q, self.dtype, c.d, n, c.H_q)
-        out = _rows("O", O, self.dtype, c.d, n, c.H_q)
+        d, heads = c.d, c.H_q
+        qr, out = _rows("q", q, self.dtype, d, n, heads), _rows("O", O, self.dtype, d, n, heads)
         k, v = self._cache("k_cache", k_cache), self._cache("v_cache", v_cache)
-        if v_cache.shape[0] != k_cache.shape[0]:
+        pages = k_cache.shape[0]
+        if v_cache.shape[0] != pages:
             raise ValueError("k_cache and v_cache must have the same pages")
-        check_vector("seq_lens", seq_lens, torch.int32, n)
-        stride = 0
+        lens, table, stride = check_vector("seq_lens", seq_lens, _int32, n), None, 0
         if page_table is not None:
-            if page_table.dtype != torch.int32 or not page_table.is_cuda or page_table.dim() != 2 or \
-                    page_table.shape[0] != n or not page_table.is_contiguous():
+            shape = page_table.shape
+            if page_table.dtype is not _int32 or not page_table.is_cuda or len(shape) != 2 or shape[0] != n or \
+                    not page_table.is_contiguous():
                 raise ValueError(f"page_table must be a contiguous CUDA tensor [{n}, pages] of int32")
-            stride = page_table.shape[1]
-        _check(self._L.syn_window_decode(self._h, qr, k, v, syn._ptr(page_table), stride, k_cache.shape[0],
-                                         syn._ptr(seq_lens), n, out, _lse(lse, n, c.H_q), syn._stream(stream)),
-               "syn_window_decode")
+            table, stride = page_table.data_ptr(), shape[1]
+        _check(self._L.syn_window_decode(self._h, qr, k, v, table, stride, pages, lens, n, out, _lse(lse, n, heads),
+                                         syn._stream(stream)), "syn_window_decode")
 
     def sync(self, stream=None) -> int:
         return int(self._L.syn_decode_sync_status(self._h, syn._stream(stream)))
