@@ -33,9 +33,11 @@ namespace window {
 constexpr int kDecThreads = 128;
 constexpr int kTileKeys = 64;
 constexpr int kRowsM = 16;         // query heads of a CTA
-constexpr int kDecStages = 3;
+constexpr int kDecStages = 2;
+constexpr int kDecCtas = 3;        // resident on an SM
+constexpr int kMaxSplits = 128;
 constexpr int kWaves = 4;          // CTAs wanted per resident slot
-constexpr int kMinTiles = 4;       // tiles of a range at least, where there are that many
+constexpr int kMinTiles = 2;       // tiles of a range at least, where there are that many
 
 struct DecParams {
     const void *q, *k, *v;
@@ -84,10 +86,11 @@ template <int D> struct DecLay {
     static constexpr int MERGE = VALID + kDecStages * kTileKeys * 4;  // [4][16] m, [4][16] l
     static constexpr int BAR = MERGE + 2 * 4 * kRowsM * 4;            // a stage's rows landed
     static constexpr int BYTES = BAR + 8 * kDecStages;
+    static_assert(BAR >= 2 * kMaxSplits * kRowsM * 4, "the join's factors take the ring's memory");
 };
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kDecThreads) window_decode_kernel(const __grid_constant__ DecParams p) {
+__global__ void __launch_bounds__(kDecThreads, kDecCtas) window_decode_kernel(const __grid_constant__ DecParams p) {
     using L = DecLay<D>;
     extern __shared__ __align__(16) uint8_t sm[];
     const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
@@ -340,16 +343,24 @@ __global__ void __launch_bounds__(kDecThreads) window_decode_kernel(const __grid
     __syncthreads();
     if (!last) return;
     __threadfence();
+    // each range's factor exp2(m - top) and the sums, all loads at once
+    float *fm = reinterpret_cast<float *>(sm), *fl = fm + kMaxSplits * kRowsM;  // [split][16]
+    for (int i = (int)threadIdx.x; i < p.splits * kRowsM; i += kDecThreads) {
+        const float *src = part + (int64_t)(i / kRowsM) * kPart + kRowsM * D + i % kRowsM;
+        fm[i] = __ldcg(src);
+        fl[i] = __ldcg(src + kRowsM);
+    }
+    __syncthreads();
     for (int row = (int)threadIdx.x / kCols; row < rows; row += kRowsAt) {
         float top = -INFINITY, sum = 0.f;
-        for (int x = 0; x < p.splits; ++x) top = fmaxf(top, __ldcg(part + (int64_t)x * kPart + kRowsM * D + row));
+        for (int x = 0; x < p.splits; ++x) top = fmaxf(top, fm[x * kRowsM + row]);
         float2 v = make_float2(0.f, 0.f);
+#pragma unroll 8
         for (int x = 0; x < p.splits; ++x) {
-            const float *src = part + (int64_t)x * kPart;
-            const float mw = __ldcg(src + kRowsM * D + row);
+            const float mw = fm[x * kRowsM + row];
             const float f = mw == -INFINITY ? 1.f : ex2(mw - top);
-            sum += __ldcg(src + kRowsM * D + kRowsM + row) * f;
-            const float2 y = __ldcg(reinterpret_cast<const float2 *>(src + row * D + col));
+            sum += fl[x * kRowsM + row] * f;
+            const float2 y = __ldcg(reinterpret_cast<const float2 *>(part + (int64_t)x * kPart + row * D + col));
             v.x = fmaf(y.x, f, v.x);
             v.y = fmaf(y.y, f, v.y);
         }
@@ -448,7 +459,7 @@ int syn_decode_plan_create(syn_decode_plan_t *out, const syn_decode_cfg_t *cfg) 
     if (e == cudaSuccess)
         e = c.d == 64 ? (pl->bf16 ? dec_prepare<64, true>() : dec_prepare<64, false>())
                       : (pl->bf16 ? dec_prepare<128, true>() : dec_prepare<128, false>());
-    pl->slots = pl->num_sms * 2;
+    pl->slots = pl->num_sms * kDecCtas;
     // at most slots * kWaves + (one a slot) partial results
     const size_t n = (size_t)c.max_seqs * c.H_kv * pl->hgroups, parts = n + (size_t)pl->slots * kWaves;
     if (e == cudaSuccess) e = cudaMalloc(&pl->d_part, parts * kRowsM * (size_t)(c.d + 2) * sizeof(float));
@@ -531,7 +542,7 @@ int syn_window_decode(syn_decode_plan_t pl, const syn_window_rows_t *q, const sy
     // no less than kMinTiles tiles of the longest sequence the table allows.
     const int64_t n = (int64_t)n_seqs * c.H_kv * pl->hgroups;
     const int64_t longest = std::min<int64_t>(p.cap, c.window + (int64_t)c.sinks);
-    const int64_t most = std::max<int64_t>(1, longest / (kTileKeys * kMinTiles));
+    const int64_t most = std::min<int64_t>(kMaxSplits, std::max<int64_t>(1, longest / (kTileKeys * kMinTiles)));
     p.splits = (int32_t)std::min<int64_t>(most, ((int64_t)pl->slots * kWaves + n - 1) / n);
     const int grid = (int)(n * p.splits);
     cudaStream_t st = static_cast<cudaStream_t>(stream);

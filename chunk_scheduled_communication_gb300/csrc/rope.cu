@@ -34,8 +34,8 @@ namespace rope {
 
 constexpr int kThreads = 256;
 constexpr int kMaxD = 256;
-constexpr int kRowsPerLane = 4;     // rows whose loads a lane has under way at long inputs (gradient: half)
-constexpr int kBlocksPerSm = 4;
+constexpr int kRowsPerLane = 4;     // rows whose loads a lane has under way at long inputs
+constexpr int kGradRowsPerLane = 3; // (gradient: of the step ahead)
 constexpr int kGradBlocksPerSm = 2; // persistent blocks of the gradient kernel
 constexpr int kTableBytes = 14 * 1024;  // cosines and sines of a block's tokens at most
 
@@ -333,7 +333,7 @@ template <typename T, int VEC, int NS, int U> __host__ __device__ constexpr int 
 // under way together, each lane's in its own slots of shared memory, so that
 // they cost no registers.
 template <typename T, int VEC, int L, int NS, int U, bool NORM>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) rope_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, NORM ? 4 : 5) rope_kernel(const __grid_constant__ Args a) {
     constexpr int G = kThreads / L;
     __shared__ Pack<T, VEC> staged[U][2 * NS * kThreads];
     extern __shared__ __align__(16) float table[];
@@ -625,7 +625,7 @@ template <typename T, int VEC, int L, int NS, int U, bool NORM> int launch_forwa
 template <typename T, int VEC, int L, int NS> int launch(syn_rope_plan_s *pl, Args &a, Kind kind, cudaStream_t st, int &grid) {
     constexpr int G = kThreads / L, kMany = VEC == 1 ? 1 : kRowsPerLane;
     if (kind == kNormGrad) {
-        constexpr int U = VEC == 1 ? 1 : kRowsPerLane / 2;
+        constexpr int U = VEC == 1 ? 1 : kGradRowsPerLane;
         a.table_tokens = 1;
         int64_t blocks = 1;
         for (int x = 0; x < a.n_tensors; ++x) {

@@ -119,6 +119,7 @@ void key_ranges(int64_t p0, int64_t p1, int64_t window, int sinks, int32_t &s_en
 void build_forward(Lists &l, const syn_window_cfg_t &c, int64_t window, int64_t q0, int64_t k0, int64_t ql, int64_t kl) {
     const int G = c.H_q / c.H_kv;
     const int64_t off = kl - ql;
+    const int bk = fwd_block(c.d);
     const bool heads = G % 2 == 0;  // the two tiles: two heads, else consecutive rows
     const int64_t step = heads ? 128 : 256;
     for (int hk = 0; hk < c.H_kv; ++hk)
@@ -142,9 +143,9 @@ void build_forward(Lists &l, const syn_window_cfg_t &c, int64_t window, int64_t 
                     continue;
                 }
                 key_ranges(off + i0, off + last, window, c.sinks, it.s_end, it.w_lo, it.k_end);
-                it.n_blk = ceil_div(it.s_end, 128) + ceil_div(it.k_end - it.w_lo, 128);
+                it.n_blk = ceil_div(it.s_end, bk) + ceil_div(it.k_end - it.w_lo, bk);
                 l.fwd.push_back(it);
-                l.fwd_cost.push_back(ceil_div(it.s_end, 32) + ceil_div(it.k_end - it.w_lo, 32) + 3);
+                l.fwd_cost.push_back(ceil_div(it.s_end, 16) + ceil_div(it.k_end - it.w_lo, 16) + 8);
             }
 }
 
@@ -439,13 +440,14 @@ int syn_window_attention(syn_window_plan_t pl, const syn_window_rows_t *Q, const
     if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return host_fail(SYN_ERR_INVALID, "lse: not aligned");
     if (nq == 0) return SYN_OK;
     FwdMaps m;
+    const uint32_t bk = (uint32_t)fwd_block(c.d);
     // without any key no item reads K or V
     const syn_window_rows_t &k = nk > 0 ? *K : *Q, &v = nk > 0 ? *V : *Q;
     const int64_t rows = nk > 0 ? nk : nq;
     const int heads = nk > 0 ? c.H_kv : c.H_q;
-    if ((rc = encode(&m.q, pl, *Q, nq, c.H_q, 128)) != SYN_OK || (rc = encode(&m.k, pl, k, rows, heads, 128)) != SYN_OK ||
-        (rc = encode(&m.k32, pl, k, rows, heads, 32)) != SYN_OK || (rc = encode(&m.v, pl, v, rows, heads, 128)) != SYN_OK ||
-        (rc = encode(&m.v32, pl, v, rows, heads, 32)) != SYN_OK)
+    if ((rc = encode(&m.q, pl, *Q, nq, c.H_q, 128)) != SYN_OK || (rc = encode(&m.k, pl, k, rows, heads, bk)) != SYN_OK ||
+        (rc = encode(&m.k16, pl, k, rows, heads, 16)) != SYN_OK || (rc = encode(&m.v, pl, v, rows, heads, bk)) != SYN_OK ||
+        (rc = encode(&m.v16, pl, v, rows, heads, 16)) != SYN_OK)
         return rc;
     FwdParams p;
     std::memset(&p, 0, sizeof(p));

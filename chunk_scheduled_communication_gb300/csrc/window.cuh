@@ -20,8 +20,8 @@ constexpr int kNoWindow = 0x3fffffff;  // "no window": above every position
 
 // Forward work item: two 128-row query tiles that read the same key blocks --
 // the same rows of two heads of a group, or consecutive rows of one head.
-// Key blocks: ceil(s_end / 128) blocks of the sinks [0, s_end), then blocks of
-// [w_lo, k_end) (keys relative to the sequence).
+// Key blocks of fwd_block(d) keys: of the sinks [0, s_end), then of [w_lo, k_end)
+// (keys relative to the sequence).
 struct alignas(16) FwdItem {
     int32_t q_row[2], head[2], n_rows[2], pos0[2];  // n_rows 0: no second tile
     int32_t kv_row0, hk, s_end, w_lo, k_end, n_blk, pad[2];
@@ -181,7 +181,7 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v,
 
 // ------------------------------------------------------------------ launches
 struct FwdMaps {
-    CUtensorMap q, k, k32, v, v32;  // 128-row boxes, and 32-row ones for narrow key blocks
+    CUtensorMap q, k, k16, v, v16;  // boxes of a tile, and of 16 rows for narrow key blocks
 };
 struct FwdParams {
     Common c;
@@ -226,6 +226,7 @@ struct SumParams {
     int32_t d;
 };
 
+int fwd_block(int d);  // keys of a key block
 int fwd_smem(int d);
 int bwd_smem(int d);
 cudaError_t fwd_prepare(int d, bool bf16);
