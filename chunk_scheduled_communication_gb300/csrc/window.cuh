@@ -67,45 +67,91 @@ struct Common {
 
 constexpr int WHERE_PIPE = 3;
 
-__device__ __forceinline__ void raise(const Common &p, int code, int where, int info) {
-    if (atomicCAS(p.err, 0, code) == 0) {
-        p.err[1] = where;
-        p.err[2] = (int)blockIdx.x;
-        p.err[3] = info;
+// Waits, arrivals and tensor-core instructions are made by whole, converged
+// warps, single-thread ones predicated: a diverged lane pays three times as
+// much for a barrier that is already complete (186 cycles against 58) and twice
+// for one that another warp arrives at (284 against 132).
+//
+// Up to a thousand polls without looking at the clock.
+__device__ __forceinline__ bool poll_bar(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, 0;\n\t"
+        "POLL_%=:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE_%=;\n\t"
+        "add.u32 n, n, 1;\n\t"
+        "setp.lt.u32 q, n, 1000;\n\t"
+        "@q bra POLL_%=;\n\t"
+        "DONE_%=:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// The rest of a wait: bounded.  A wait that runs out records SYN_ERR_TIMEOUT and
+// sets `abort`, after which no wait lasts; the warp goes on, with wrong results
+// but within its buffers, to the end of its loop.
+__device__ __forceinline__ void wait_long(uint32_t bar, uint32_t parity, volatile int *abort, const Common &p) {
+    const uint64_t t0 = ptx::globaltimer();
+    while (!poll_bar(bar, parity)) {
+        if (abort != nullptr && *abort != 0) return;
+        const bool late = ptx::globaltimer() - t0 > p.timeout_ns;
+        if (late && atomicCAS(p.err, 0, SYN_ERR_TIMEOUT) == 0) {
+            p.err[1] = WHERE_PIPE;
+            p.err[2] = (int)blockIdx.x;
+            p.err[3] = (int)bar;
+        }
+        if (late || *reinterpret_cast<volatile int32_t *>(p.err) != 0) {
+            if (abort == nullptr) {
+                if (late) return;
+                continue;
+            }
+            *abort = 1;
+            return;
+        }
     }
 }
 
-// Bounded wait on a shared-memory barrier phase; false on abort or timeout.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort, const Common &p) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = ptx::globaltimer();
-    for (uint32_t n = 1;; ++n) {
-        if (ptx::mbar_try_wait(bar, parity)) return true;
-        if (*abort) return false;
-        if ((n & 63u) == 0u) {
-            if (*reinterpret_cast<volatile int32_t *>(p.err) != 0) {
-                *abort = 1;
-                return false;
-            }
-            if (ptx::globaltimer() - t0 > p.timeout_ns) {
-                raise(p, SYN_ERR_TIMEOUT, WHERE_PIPE, (int)bar);
-                *abort = 1;
-                return false;
-            }
-        }
-    }
+// Bounded wait of a warp on a shared-memory barrier phase.
+__device__ __forceinline__ void wait_bar(uint32_t bar, uint32_t parity, volatile int *abort, const Common &p) {
+    if (!poll_bar(bar, parity)) wait_long(bar, parity, abort, p);
+    __syncwarp();
 }
 
 // Wait used while draining on the way out: ignores the abort flag.
 __device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity, const Common &p) {
-    const uint64_t t0 = ptx::globaltimer();
-    for (uint32_t n = 0;; ++n) {
-        if (ptx::mbar_try_wait(bar, parity)) return;
-        if ((n & 63u) == 63u && ptx::globaltimer() - t0 > p.timeout_ns) {
-            raise(p, SYN_ERR_TIMEOUT, WHERE_PIPE, (int)bar);
-            return;
-        }
-    }
+    wait_long(bar, parity, nullptr, p);
+    __syncwarp();
+}
+
+// One lane's arrival, MMA or commit (`on`: this lane's)
+__device__ __forceinline__ void arrive_if(uint32_t on, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%1];\n\t}" ::"r"(on), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void umma_if(uint32_t on, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(adesc), "l"(bdesc),
+        "r"(idesc), "r"(accumulate), "r"(on) : "memory");
+}
+__device__ __forceinline__ void umma_ts_if(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc),
+        "r"(idesc), "r"(accumulate), "r"(on) : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t on, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(on), "r"(bar) : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -144,6 +190,31 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// Bits [0, n) of a 32-bit word whose first bit is number `at`
+__device__ __forceinline__ uint32_t bits_below(int n, int at) {
+    const int m = n - at;
+    return m <= 0 ? 0u : m >= 32 ? 0xffffffffu : (1u << m) - 1u;
+}
+// v where bit `bit` of the mask is set, else `other`: a select (a condition in C
+// became a branch for each element, each of them diverging)
+template <int BIT> __device__ __forceinline__ uint32_t keep_if(uint32_t mask, uint32_t v, uint32_t other) {
+    uint32_t r;
+    asm("{\n\t.reg .pred p;\n\t.reg .b32 t;\n\t"
+        "and.b32 t, %1, %4;\n\t"
+        "setp.ne.u32 p, t, 0;\n\t"
+        "selp.b32 %0, %2, %3, p;\n\t}"
+        : "=r"(r)
+        : "r"(mask), "r"(v), "r"(other), "n"(1u << BIT));
+    return r;
+}
+// v[K ..]: `other` where the mask's bit is not set
+template <int K, int N> struct MaskRow {
+    static __device__ __forceinline__ void apply(uint32_t (&v)[N], const uint32_t (&mask)[(N + 31) / 32], uint32_t other) {
+        v[K] = keep_if<K % 32>(mask[K / 32], v[K], other);
+        if constexpr (K + 1 < N) MaskRow<K + 1, N>::apply(v, mask, other);
+    }
+};
+
 // Two fp32 values rounded to the 16-bit type, the lower in the low half
 template <bool BF16> __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     if (BF16) {
@@ -166,6 +237,19 @@ __device__ __forceinline__ uint64_t kmajor_desc(uint32_t tile, uint32_t box, int
 // rows 16kk .. 16kk+15 (2048 bytes on), the boxes `box` apart.
 __device__ __forceinline__ uint64_t mnmajor_desc(uint32_t tile, uint32_t box, int kk) {
     return ptx::sdesc(tile + (uint32_t)kk * 2048u, box, 1024, ptx::kSwizzle128B);
+}
+
+// The same descriptors from their two words: the upper is the same for all (8-row
+// atoms 1024 bytes apart, version 1, 128-byte swizzle), the lower holds address
+// and box distance, and a later slice of the tile only adds to the address.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t tile, uint32_t lbo_bytes) {
+    return ((tile & 0x3FFFFu) >> 4) | ((lbo_bytes >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t desc_at(uint32_t lo, int bytes) {
+    constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (ptx::kSwizzle128B << 29);
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo + (uint32_t)(bytes >> 4)), "r"(hi));
+    return d;
 }
 
 // Zero rows [r0, r1) of a tile of D columns (one warp, generic proxy); the

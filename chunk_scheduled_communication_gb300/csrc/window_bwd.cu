@@ -120,6 +120,16 @@ template <bool KEYS> struct Walk {
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 96;"); }
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 200;"); }
 
+// Probabilities and score gradients of columns 2K, 2K + 1 ..: 0 where not seen
+template <int K> struct PairRow {
+    static __device__ __forceinline__ void apply(uint32_t (&p)[32], uint32_t (&d)[32], const uint32_t (&seen)[2]) {
+        const uint32_t both = keep_if<2 * K % 32>(seen[K / 16], 0x0000ffffu, 0u) | keep_if<2 * K % 32 + 1>(seen[K / 16], 0xffff0000u, 0u);
+        p[K] &= both;
+        d[K] &= both;
+        if constexpr (K < 31) PairRow<K + 1>::apply(p, d, seen);
+    }
+};
+
 // 32 accumulator columns of this thread's row to 16-bit (dst) or fp32 (part)
 template <bool BF16>
 __device__ __forceinline__ void store_cols(uint32_t taddr, uint16_t *dst, float *part, float scale) {
@@ -182,21 +192,23 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
         Blk b = {};
         if (warp == 0) {
             // ================= TMA producer =================
-            if (lane == 0) {
-                uint32_t g = 0, ic = 0;
-                for (; wk.next(p, b); ++g) {
-                    if (b.first) {
-                        if (!wait_bar(bar(B_XE), (ic & 1u) ^ 1u, abort, c)) break;
+            uint32_t g = 0, ic = 0;
+            for (; wk.next(p, b); ++g) {
+                if (b.first) {
+                    wait_bar(bar(B_XE), (ic & 1u) ^ 1u, abort, c);
+                    if (lane == 0) {
                         const int hx = KEYS ? wk.it->hk : b.h;
                         ptx::mbar_arrive_expect_tx(bar(B_XF), 2 * L::kTileX);
                         for (int x = 0; x < D / 64; ++x) {
                             ptx::tma_load_3d(sbase + L::X + (uint32_t)(x * kBoxX), &m.x, bar(B_XF), x * 64, hx, wk.it->row0);
                             ptx::tma_load_3d(sbase + L::Y + (uint32_t)(x * kBoxX), &m.y, bar(B_XF), x * 64, hx, wk.it->row0);
                         }
-                        ++ic;
                     }
-                    const int s = (int)(g % kStages);
-                    if (!wait_bar(bar(B_UE + s), ((g / kStages) & 1u) ^ 1u, abort, c)) break;
+                    ++ic;
+                }
+                const int s = (int)(g % kStages);
+                wait_bar(bar(B_UE + s), ((g / kStages) & 1u) ^ 1u, abort, c);
+                if (lane == 0) {
                     const uint32_t u = sbase + (uint32_t)(L::RING + s * L::kStage);
                     const int hu = KEYS ? b.h : wk.it->hk, row = wk.it->stream0 + b.start;
                     ptx::mbar_arrive_expect_tx(bar(B_UF + s), L::kStage + (KEYS ? 512 : 0));
@@ -210,11 +222,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
                         ptx::bulk_g2s(sbase + (uint32_t)(L::STAT + s * 512 + 256), p.ndelta + o, 256, bar(B_UF + s));
                     }
                 }
-                // every load issued must land before the CTA exits
-                if (ic > 0) drain_bar(bar(B_XF), (ic - 1u) & 1u, c);
-                for (uint32_t s = 0; s < kStages; ++s)
-                    if (g > s) drain_bar(bar(B_UF + (int)s), ((g - 1u - s) / kStages) & 1u, c);
+                __syncwarp();
             }
+            // every load issued must land before the CTA exits
+            if (ic > 0) drain_bar(bar(B_XF), (ic - 1u) & 1u, c);
+            for (uint32_t s = 0; s < kStages; ++s)
+                if (g > s) drain_bar(bar(B_UF + (int)s), ((g - 1u - s) / kStages) & 1u, c);
         } else if (warp == 2) {
             // ================= streaming rows past the end =================
             // (asked by the issuer, which follows every block: this warp sees only
@@ -223,8 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
             for (uint32_t g = 0; wk.next(p, b); ++g) {
                 if (b.valid >= kBU) continue;
                 const int s = (int)(g % kStages);
-                const bool w = wait_bar(bar(B_ZR), nz++ & 1u, abort, c);
-                if (!__all_sync(0xffffffffu, w)) break;
+                wait_bar(bar(B_ZR), nz++ & 1u, abort, c);
                 zero_rows<D>(sm + L::RING + s * L::kStage, kBoxU, b.valid, kBU, lane);
                 zero_rows<D>(sm + L::RING + s * L::kStage + L::kTileU, kBoxU, b.valid, kBU, lane);
                 ptx::fence_proxy_async_smem();
@@ -233,72 +245,70 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
             }
         } else if (warp == 1) {
             // ================= MMA issuer =================
-            if (lane == 0) {
-                constexpr uint32_t id_s = ptx::idesc_16bit_f32(BF16, 128, kBU, false);
-                constexpr uint32_t id_a = ptx::idesc_16bit_f32(BF16, 128, D, true);
-                uint32_t nz = 0, ic = 0;
-                // sums of block g: dX (+)= dS U, and dY (+)= P W in the dK, dV form
-                auto sums = [&](uint32_t g, const Blk &k, uint32_t item) -> bool {
-                    const int s = (int)(g % kStages);
-                    const uint32_t buf = tmem + (g & 1u) * 128u;
-                    if (!wait_bar(bar(B_PF + (int)(g & 1u)), (g >> 1) & 1u, abort, c)) return false;
-                    if (k.first) {  // the place's previous output has been read
-                        const bool w = KEYS ? item == 0 || wait_bar(bar(B_OE), (item - 1u) & 1u, abort, c)
-                                            : item < 2 || wait_bar(bar(B_OE + (int)(item & 1u)), ((item >> 1) - 1u) & 1u, abort, c);
-                        if (!w) return false;
-                    }
-                    ptx::tc_fence_after();
-                    const uint32_t u = sbase + (uint32_t)(L::RING + s * L::kStage);
+            constexpr uint32_t id_s = ptx::idesc_16bit_f32(BF16, 128, kBU, false);
+            constexpr uint32_t id_a = ptx::idesc_16bit_f32(BF16, 128, D, true);
+            const uint32_t x_d = desc_lo(sbase + L::X, 16), y_d = desc_lo(sbase + L::Y, 16);
+            const uint32_t u_k = desc_lo(sbase + L::RING, 16), u_m = desc_lo(sbase + L::RING, kBoxU);
+            uint32_t nz = 0, ic = 0;
+            // sums of block g: dX (+)= dS U, and dY (+)= P W in the dK, dV form
+            auto sums = [&](uint32_t g, const Blk &k, uint32_t item) {
+                const int s = (int)(g % kStages);
+                const uint32_t buf = tmem + (g & 1u) * 128u;
+                if (k.first) {  // the place's previous output has been read
+                    if (KEYS && item > 0) wait_bar(bar(B_OE), (item - 1u) & 1u, abort, c);
+                    if (!KEYS && item > 1) wait_bar(bar(B_OE + (int)(item & 1u)), ((item >> 1) - 1u) & 1u, abort, c);
+                }
+                wait_bar(bar(B_PF + (int)(g & 1u)), (g >> 1) & 1u, abort, c);
+                ptx::tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t u = u_m + (uint32_t)(s * L::kStage >> 4);
                     const uint32_t dx = tmem + 256u + (KEYS ? 0u : (item & 1u) * 128u);
 #pragma unroll
                     for (int kk = 0; kk < kBU / 16; ++kk) {
                         const uint32_t acc = (kk != 0 || !k.first) ? 1u : 0u;
-                        if (KEYS)
-                            ptx::umma_bf16_ts(tmem + 384u, buf + (uint32_t)(kk * 8), mnmajor_desc(u + L::kTileU, kBoxU, kk), id_a, acc);
-                        ptx::umma_bf16_ts(dx, buf + 64u + (uint32_t)(kk * 8), mnmajor_desc(u, kBoxU, kk), id_a, acc);
+                        if (KEYS) ptx::umma_bf16_ts(tmem + 384u, buf + (uint32_t)(kk * 8), desc_at(u, L::kTileU + kk * 2048), id_a, acc);
+                        ptx::umma_bf16_ts(dx, buf + 64u + (uint32_t)(kk * 8), desc_at(u, kk * 2048), id_a, acc);
                     }
                     ptx::umma_commit(bar(B_DN + (int)(g & 1u)));
                     ptx::umma_commit(bar(B_UE + s));
                     if (k.last) ptx::umma_commit(bar(B_AF));
-                    return true;
-                };
-                Blk prev = {};
-                uint32_t g = 0;
-                bool ok = true;
-                for (; ok && wk.next(p, b); ++g) {
-                    if (b.first) {
-                        if (!wait_bar(bar(B_XF), ic & 1u, abort, c)) { ok = false; break; }
-                        ++ic;
-                    }
-                    const int s = (int)(g % kStages);
-                    if (!wait_bar(bar(B_UF + s), (g / kStages) & 1u, abort, c)) { ok = false; break; }
-                    if (b.valid < kBU) {
-                        ptx::mbar_arrive(bar(B_ZR));
-                        if (!wait_bar(bar(B_UZ), nz & 1u, abort, c)) { ok = false; break; }
-                        ++nz;
-                    }
-                    // buffer g & 1: P, dS of block g - 2 read
-                    if (g > 1 && !wait_bar(bar(B_DN + (int)(g & 1u)), ((g >> 1) - 1u) & 1u, abort, c)) { ok = false; break; }
-                    ptx::tc_fence_after();
-                    const uint32_t u = sbase + (uint32_t)(L::RING + s * L::kStage);
+                }
+                __syncwarp();
+            };
+            Blk prev = {};
+            uint32_t g = 0;
+            for (; wk.next(p, b); ++g) {
+                if (b.first) wait_bar(bar(B_XF), ic++ & 1u, abort, c);
+                const int s = (int)(g % kStages);
+                wait_bar(bar(B_UF + s), (g / kStages) & 1u, abort, c);
+                if (b.valid < kBU) {
+                    if (lane == 0) ptx::mbar_arrive(bar(B_ZR));
+                    wait_bar(bar(B_UZ), nz++ & 1u, abort, c);
+                }
+                // buffer g & 1: P, dS of block g - 2 read
+                if (g > 1) wait_bar(bar(B_DN + (int)(g & 1u)), ((g >> 1) - 1u) & 1u, abort, c);
+                ptx::tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t u = u_k + (uint32_t)(s * L::kStage >> 4);
                     const uint32_t buf = tmem + (g & 1u) * 128u;
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        ptx::umma_bf16(buf, kmajor_desc(sbase + L::X, kBoxX, kk), kmajor_desc(u, kBoxU, kk), id_s, kk != 0 ? 1u : 0u);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        ptx::umma_bf16(buf + 64u, kmajor_desc(sbase + L::Y, kBoxX, kk), kmajor_desc(u + L::kTileU, kBoxU, kk), id_s,
-                                       kk != 0 ? 1u : 0u);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const int ox = (kk >> 2) * kBoxX + (kk & 3) * 32, ou = (kk >> 2) * kBoxU + (kk & 3) * 32;
+                        ptx::umma_bf16(buf, desc_at(x_d, ox), desc_at(u, ou), id_s, kk != 0 ? 1u : 0u);
+                        ptx::umma_bf16(buf + 64u, desc_at(y_d, ox), desc_at(u, L::kTileU + ou), id_s, kk != 0 ? 1u : 0u);
+                    }
                     ptx::umma_commit(bar(B_SF + (int)(g & 1u)));
                     if (b.last) ptx::umma_commit(bar(B_XE));
-                    if (g > 0) ok = sums(g - 1u, prev, b.first ? ic - 2u : ic - 1u);
-                    prev = b;
                 }
-                if (ok && g > 0) sums(g - 1u, prev, ic - 1u);
-                // every MMA issued must complete before TMEM is released
-                ptx::umma_commit(bar(B_DRAIN));
-                drain_bar(bar(B_DRAIN), 0, c);
+                __syncwarp();
+                if (g > 0) sums(g - 1u, prev, b.first ? ic - 2u : ic - 1u);
+                prev = b;
             }
+            if (g > 0) sums(g - 1u, prev, ic - 1u);
+            // every MMA issued must complete before TMEM is released
+            if (lane == 0) ptx::umma_commit(bar(B_DRAIN));
+            __syncwarp();
+            drain_bar(bar(B_DRAIN), 0, c);
         }
     } else {
         regs_inc();
@@ -324,9 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
             }
             if ((g & 1u) == (uint32_t)wg) {
                 const int s = (int)(g % kStages);
-                bool w = wait_bar(bar(B_SF + wg), (g >> 1) & 1u, abort, c);
-                if (KEYS) w = w && wait_bar(bar(B_UF + s), (g / kStages) & 1u, abort, c);  // the statistics
-                if (!__all_sync(0xffffffffu, w)) break;
+                wait_bar(bar(B_SF + wg), (g >> 1) & 1u, abort, c);
+                if (KEYS) wait_bar(bar(B_UF + s), (g / kStages) & 1u, abort, c);  // the statistics
                 ptx::tc_fence_after();
                 uint32_t sv[64], dv[64];
 #pragma unroll
@@ -369,18 +378,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
                     float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
                     unf2(mul2(f2(p0, p1), add2(f2(__uint_as_float(dv[k]), __uint_as_float(dv[k + 1])), f2(d.x, d.y))), y0, y1);
                     unf2(mul2(f2(p2, p3), add2(f2(__uint_as_float(dv[k + 2]), __uint_as_float(dv[k + 3])), f2(d.z, d.w))), y2, y3);
-                    if (masked) {
-                        const bool n0 = k >= hi || (k < lo && k >= sk), n1 = k + 1 >= hi || (k + 1 < lo && k + 1 >= sk);
-                        const bool n2 = k + 2 >= hi || (k + 2 < lo && k + 2 >= sk), n3 = k + 3 >= hi || (k + 3 < lo && k + 3 >= sk);
-                        if (n0) p0 = y0 = 0.f;
-                        if (n1) p1 = y1 = 0.f;
-                        if (n2) p2 = y2 = 0.f;
-                        if (n3) p3 = y3 = 0.f;
-                    }
                     pk[k / 2] = pack16<BF16>(p0, p1);
                     pk[k / 2 + 1] = pack16<BF16>(p2, p3);
                     dk[k / 2] = pack16<BF16>(y0, y1);
                     dk[k / 2 + 1] = pack16<BF16>(y2, y3);
+                }
+                if (masked) {  // (pairs of 16 bits: a word's mask has both halves)
+                    uint32_t seen[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        seen[x] = bits_below(hi, 32 * x) & (~bits_below(lo, 32 * x) | bits_below(sk, 32 * x));
+                    PairRow<0>::apply(pk, dk, seen);
                 }
                 if (KEYS) ptx::tmem_st_32x32b_x32(ts, pk);
                 ptx::tmem_st_32x32b_x32(ts + 64u, dk);
@@ -390,8 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
                 if (lane == 0) ptx::mbar_arrive(bar(B_PF + wg));
             }
             if (b.last) {  // the item's sums are complete
-                const bool w = wait_bar(bar(B_AF), item & 1u, abort, c);
-                if (!__all_sync(0xffffffffu, w)) break;
+                wait_bar(bar(B_AF), item & 1u, abort, c);
                 ptx::tc_fence_after();
                 const bool mine = row < it.n_rows;
                 const int64_t r = it.row0 + row;

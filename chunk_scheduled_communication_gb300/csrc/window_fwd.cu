@@ -9,19 +9,24 @@
 // cost a fifth of a block.  The online softmax keeps a running maximum and sum
 // per row, one pass over the keys:
 //
-//   warp 0      TMA producer: an item's Q tiles, each block's K and V (rings)
-//   warps 1, 3  MMA issuers, one per tile: S_t = Q_t.K^T, then O_t += P_t.V
-//   warp 2      zeroes V rows past the end of a block's keys: their probabilities
-//               are 0, and 0 times another sequence's inf or NaN is not
-//   warps 4-7   softmax of tile 0 (one query row per thread, its TMEM lane)
-//   warps 8-11  softmax of tile 1
+//   warp 0        TMA producer: an item's Q tiles, each block's K and V (a ring)
+//   warps 1, 2    issue S_t = Q_t.K^T of tile 0, 1
+//   warps 3, 4    issue O_t += P_t.V of tile 0, 1
+//   warp 5        zeroes V rows past the end of a block's keys: their probabilities
+//                 are 0, and 0 times another sequence's inf or NaN is not
+//   warps 8-11    softmax of tile 0 (one query row per thread, its TMEM lane)
+//   warps 12-15   softmax of tile 1
+//
+// Each product has an issuing warp of its own because a warp's waits, commits
+// and branches cost more than the tensor pipe needs for a block: one issuer a
+// tile, or one for all, left the pipe idle for a third of the time.
 //
 // TMEM (512 columns) holds each tile's scores, probabilities (16-bit, half as
 // many columns) and output side by side, so that the scores of block g+1 are
 // computed while the softmax works on block g: it frees the score columns as
 // soon as it has loaded them, and nothing waits for P.V but the next block's
 // probabilities.  With D 128 that fits blocks of 80 keys (80 + 40 + 128 columns
-// a tile), with D 64 blocks of 128 (128 + 64 + 64).  The reference maximum of
+// a tile), and more than 80 scores a thread spill registers.  The reference maximum of
 // the exponentials may lag the row's by up to 8 (log2 units), so the
 // accumulator is rescaled only when a block raises it by more.
 #include "window.cuh"
@@ -33,31 +38,29 @@ namespace {
 
 constexpr int kBQ = 128, kTiles = 2;
 constexpr int kBoxQ = kBQ * 128;  // 128 rows x 128 bytes
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kSmemItems = 48;   // items of the CTA's list kept in shared memory
 constexpr float kRescale = 8.f;
 
 constexpr int kMaxStages = 4;
 enum {
     B_QF = 0,                     // the item's Q tiles landed
-    B_QE = 1,                     // Q tiles read by the item's last Q.K^T (one commit per issuer)
-    B_KF = 2,                     // K stage landed
-    B_KE = B_KF + kMaxStages,     // K stage consumed (one commit per issuer)
-    B_VF = B_KE + kMaxStages,     // V stage landed
-    B_VE = B_VF + kMaxStages,     // V stage consumed (one commit per issuer)
-    B_SF = B_VE + kMaxStages,     // tile t's scores written (2)
+    B_QE = 1,                     // Q tiles read by the item's last Q.K^T (one commit per tile)
+    B_KF = 2,                     // stage landed: a block's K and V
+    B_KE = B_KF + kMaxStages,     // stage consumed (one commit per tile, after its P.V)
+    B_SF = B_KE + kMaxStages,     // tile t's scores written (2)
     B_SL = B_SF + 2,              // tile t's scores loaded into registers (2)
     B_PF = B_SL + 2,              // tile t's probabilities written (2)
     B_PV = B_PF + 2,              // tile t's P.V done (2)
     B_OE = B_PV + 2,              // tile t's accumulator read out (2)
-    B_DRAIN = B_OE + 2,           // every MMA of tile t's issuer completed (2)
-    B_ZR = B_DRAIN + 2,           // a V block with rows past its keys landed (asked by both issuers)
+    B_DRAIN = B_OE + 2,           // every MMA of an issuer completed (4)
+    B_ZR = B_DRAIN + 4,           // a block with V rows past its keys landed (asked by both P.V issuers)
     B_VZ = B_ZR + 1,              // its rows past the keys zeroed
     N_BAR = B_VZ + 1
 };
 
 template <int D> struct Lay {
-    static constexpr int kBK = D == 128 ? 80 : 128;  // keys of a block
+    static constexpr int kBK = 80;  // keys of a block
     static constexpr int kStages = D == 128 ? 3 : 4;
     static constexpr int kBoxK = kBK * 128;
     static constexpr int kTileQ = kBQ * D * 2, kTileK = kBK * D * 2;
@@ -75,46 +78,35 @@ template <int D> struct Lay {
     __host__ __device__ static constexpr uint32_t O(int t) { return 256u + (uint32_t)(D * t); }
 };
 
-// One key block of an item
+// A key block: first key, end of its valid keys, keys computed (a multiple of 16)
 struct Blk {
-    int kv0, kend, nk;  // first key, end of its valid keys, keys computed (a multiple of 16)
-    bool first, last;
+    int kv0, kend, nk;
 };
 
-// The CTA's walk over its items' blocks; every role makes the same one.
-template <int kBK> struct Walk {
-    int i, end, b;
-    const FwdItem *list;  // shared-memory copy
-    const FwdItem *rest;  // global list
-    const FwdItem *it;
-    __device__ __forceinline__ void load() {
-        it = i < kSmemItems ? list + i : rest + i;  // (read only while i < end)
-        b = 0;
+// Block b of an item, from block b - 1 (b > 0)
+template <int kBK> __device__ __forceinline__ void step(Blk &k, int b, int n_sink, const FwdItem &it) {
+    if (b == n_sink) {
+        k.kv0 = it.w_lo;
+        k.kend = it.k_end;
+    } else if (b == 0) {
+        k.kv0 = 0;
+        k.kend = it.s_end;
+    } else {
+        k.kv0 += kBK;
     }
-    __device__ __forceinline__ void init(const FwdParams &p, const FwdItem *smem_items) {
-        const int b0 = p.begin[blockIdx.x];
-        list = smem_items;
-        rest = p.items + b0;
-        i = 0;
-        end = p.begin[blockIdx.x + 1] - b0;
-        load();
-    }
-    // the next block; `it` is its item until the next call
-    __device__ __forceinline__ bool next(Blk &k) {
-        if (i < end && b == it->n_blk) {
-            ++i;
-            load();
+    k.nk = min(kBK, (k.kend - k.kv0 + 15) & ~15);
+}
+
+// Every role walks the CTA's items and their blocks: g counts the blocks, `item`
+// the items, and stage and phase follow g.
+struct Ring {
+    int s = 0;
+    uint32_t phase = 0;
+    template <int kStages> __device__ __forceinline__ void next() {
+        if (++s == kStages) {
+            s = 0;
+            phase ^= 1u;
         }
-        if (i >= end) return false;
-        const int n_sink = (it->s_end + kBK - 1) / kBK;
-        const bool sink = b < n_sink;
-        k.kv0 = sink ? b * kBK : it->w_lo + (b - n_sink) * kBK;
-        k.kend = sink ? it->s_end : it->k_end;
-        k.nk = min(kBK, (k.kend - k.kv0 + 15) & ~15);
-        k.first = b == 0;
-        ++b;
-        k.last = b == it->n_blk;
-        return true;
     }
 };
 
@@ -139,11 +131,10 @@ template <bool BF16, int D> __device__ __forceinline__ void store_row(void *dst_
     }
 }
 
-// Register split: the launch gives 168 a thread (384 threads); the producer,
-// issuer and zeroing warps give theirs down to 96, the softmax warps take 200:
-// 128 * 96 + 256 * 200 = 63,488 of 64,512.
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 96;"); }
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 200;"); }
+// Register split: the launch gives 128 a thread (512 threads); the first eight
+// warps keep 72, the softmax warps take 184: 256 * 72 + 256 * 184 = 65,536.
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 184;"); }
 
 template <bool B> struct Bool {
     static constexpr bool value = B;
@@ -168,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     if (threadIdx.x == 0) {
         *abort = 0;
         for (int i = 0; i < N_BAR; ++i) {
-            const bool pair = i == B_QE || i == B_ZR || (i >= B_KE && i < B_KE + kMaxStages) || (i >= B_VE && i < B_VE + kMaxStages);
+            const bool pair = i == B_QE || i == B_ZR || (i >= B_KE && i < B_KE + kMaxStages);
             const bool warps = i == B_SL || i == B_SL + 1 || i == B_PF || i == B_PF + 1 || i == B_OE || i == B_OE + 1;
             ptx::mbar_init(bar(i), pair ? kTiles : warps ? 4 : 1);
         }
@@ -191,144 +182,136 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     const uint32_t tmem = *tmem_slot;
     const uint32_t sQ = sbase + L::Q, sK = sbase + L::K, sV = sbase + L::V;
 
-    if (warp < 4) {
+    const int first_item = p.begin[blockIdx.x], n_items = p.begin[blockIdx.x + 1] - first_item;
+    auto item_at = [&](int i) -> const FwdItem & { return i < kSmemItems ? items[i] : p.items[first_item + i]; };
+    const uint32_t one = lane == 0 ? 1u : 0u;
+
+    if (warp < 8) {
         regs_dec();
-        Walk<kBK> wk;
-        wk.init(p, items);
+        Ring r;
         Blk b = {};
+        uint32_t g = 0;
         if (warp == 0) {
             // ================= TMA producer =================
-            if (lane == 0) {
-                uint32_t g = 0, ic = 0, nk = 0, nv = 0;
-                auto load = [&](uint32_t dst, const CUtensorMap *full, const CUtensorMap *narrow, uint32_t br, int row) {
-                    ptx::mbar_arrive_expect_tx(br, (uint32_t)(b.nk * D * 2));
-                    for (int x = 0; x < D / 64; ++x) {
-                        if (b.nk == kBK) {
-                            ptx::tma_load_3d(dst + (uint32_t)(x * L::kBoxK), full, br, x * 64, wk.it->hk, row);
-                        } else {
-                            for (int r = 0; r < b.nk; r += 16)
-                                ptx::tma_load_3d(dst + (uint32_t)(x * L::kBoxK + r * 128), narrow, br, x * 64, wk.it->hk, row + r);
+            for (int i = 0; i < n_items; ++i) {
+                const FwdItem &it = item_at(i);
+                const int n_blk = it.n_blk, n_sink = (it.s_end + kBK - 1) / kBK, hk = it.hk, row0 = it.kv_row0;
+                wait_bar(bar(B_QE), ((uint32_t)i & 1u) ^ 1u, abort, c);
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(bar(B_QF), kTiles * L::kTileQ);
+                    for (int t = 0; t < kTiles; ++t)
+                        for (int x = 0; x < D / 64; ++x)
+                            ptx::tma_load_3d(sQ + (uint32_t)(t * L::kTileQ + x * kBoxQ), &m.q, bar(B_QF), x * 64, it.head[t],
+                                             it.q_row[t]);
+                }
+                __syncwarp();
+                for (int k = 0; k < n_blk; ++k, ++g, r.next<kStages>()) {
+                    step<kBK>(b, k, n_sink, it);
+                    wait_bar(bar(B_KE + r.s), r.phase ^ 1u, abort, c);
+                    if (lane == 0) {
+                        const uint32_t br = bar(B_KF + r.s), dk = sK + (uint32_t)(r.s * L::kTileK), dv = sV + (uint32_t)(r.s * L::kTileK);
+                        ptx::mbar_arrive_expect_tx(br, (uint32_t)(2 * b.nk * D * 2));
+                        for (int x = 0; x < D / 64; ++x) {
+                            const uint32_t o = (uint32_t)(x * L::kBoxK);
+                            if (b.nk == kBK) {
+                                ptx::tma_load_3d(dk + o, &m.k, br, x * 64, hk, row0 + b.kv0);
+                                ptx::tma_load_3d(dv + o, &m.v, br, x * 64, hk, row0 + b.kv0);
+                            } else {
+                                for (int y = 0; y < b.nk; y += 16) {
+                                    ptx::tma_load_3d(dk + o + (uint32_t)(y * 128), &m.k16, br, x * 64, hk, row0 + b.kv0 + y);
+                                    ptx::tma_load_3d(dv + o + (uint32_t)(y * 128), &m.v16, br, x * 64, hk, row0 + b.kv0 + y);
+                                }
+                            }
                         }
                     }
-                };
-                for (; wk.next(b); ++g) {
-                    if (b.first) {
-                        if (!wait_bar(bar(B_QE), (ic & 1u) ^ 1u, abort, c)) break;
-                        ptx::mbar_arrive_expect_tx(bar(B_QF), kTiles * L::kTileQ);
-                        for (int t = 0; t < kTiles; ++t)
-                            for (int x = 0; x < D / 64; ++x)
-                                ptx::tma_load_3d(sQ + (uint32_t)(t * L::kTileQ + x * kBoxQ), &m.q, bar(B_QF), x * 64,
-                                                 wk.it->head[t], wk.it->q_row[t]);
-                        ++ic;
-                    }
-                    const int s = (int)(g % kStages);
-                    const uint32_t ph = (g / kStages) & 1u;
-                    const int row = wk.it->kv_row0 + b.kv0;
-                    if (!wait_bar(bar(B_KE + s), ph ^ 1u, abort, c)) break;
-                    load(sK + (uint32_t)(s * L::kTileK), &m.k, &m.k16, bar(B_KF + s), row);
-                    ++nk;
-                    if (!wait_bar(bar(B_VE + s), ph ^ 1u, abort, c)) break;
-                    load(sV + (uint32_t)(s * L::kTileK), &m.v, &m.v16, bar(B_VF + s), row);
-                    ++nv;
-                }
-                // every load issued must land before the CTA exits
-                if (ic > 0) drain_bar(bar(B_QF), (ic - 1u) & 1u, c);
-                for (uint32_t s = 0; s < kStages; ++s) {
-                    if (nk > s) drain_bar(bar(B_KF + (int)s), ((nk - 1u - s) / kStages) & 1u, c);
-                    if (nv > s) drain_bar(bar(B_VF + (int)s), ((nv - 1u - s) / kStages) & 1u, c);
+                    __syncwarp();
                 }
             }
-        } else if (warp == 2) {
+            // every load issued must land before the CTA exits
+            if (n_items > 0) drain_bar(bar(B_QF), (uint32_t)(n_items - 1) & 1u, c);
+            for (uint32_t s = 0; s < kStages; ++s)
+                if (g > s) drain_bar(bar(B_KF + (int)s), ((g - 1u - s) / kStages) & 1u, c);
+        } else if (warp <= 2) {
+            // ================= S_t = Q_t . K^T =================
+            const int t = warp - 1;
+            const uint32_t d_s = tmem + L::S(t), q_d = desc_lo(sQ + (uint32_t)(t * L::kTileQ), 16), k_d0 = desc_lo(sK, 16);
+            for (int i = 0; i < n_items; ++i) {
+                const FwdItem &it = item_at(i);
+                const int n_blk = it.n_blk, n_sink = (it.s_end + kBK - 1) / kBK;
+                wait_bar(bar(B_QF), (uint32_t)i & 1u, abort, c);
+                for (int k = 0; k < n_blk; ++k, ++g, r.next<kStages>()) {
+                    step<kBK>(b, k, n_sink, it);
+                    const uint32_t idesc = ptx::idesc_16bit_f32(BF16, 128, b.nk, false);
+                    const uint32_t k_d = k_d0 + (uint32_t)(r.s * L::kTileK >> 4);
+                    wait_bar(bar(B_KF + r.s), r.phase, abort, c);
+                    if (g > 0) wait_bar(bar(B_SL + t), (g - 1u) & 1u, abort, c);  // the softmax has loaded S of block g - 1
+                    ptx::tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        umma_if(one, d_s, desc_at(q_d, (kk >> 2) * kBoxQ + (kk & 3) * 32),
+                                desc_at(k_d, (kk >> 2) * L::kBoxK + (kk & 3) * 32), idesc, kk != 0 ? 1u : 0u);
+                    commit_if(one, bar(B_SF + t));
+                    if (k == n_blk - 1) commit_if(one, bar(B_QE));
+                }
+            }
+            // every MMA issued must complete before TMEM is released
+            commit_if(one, bar(B_DRAIN + t));
+            drain_bar(bar(B_DRAIN + t), 0, c);
+        } else if (warp <= 4) {
+            // ================= O_t (+)= P_t . V =================
+            const int t = warp - 3;
+            const uint32_t a_p = tmem + L::P(t), d_o = tmem + L::O(t), v_d0 = desc_lo(sV, L::kBoxK);
+            constexpr uint32_t idesc = ptx::idesc_16bit_f32(BF16, 128, D, true);
+            uint32_t nz = 0;  // zeroed blocks so far
+            for (int i = 0; i < n_items; ++i) {
+                const FwdItem &it = item_at(i);
+                const int n_blk = it.n_blk, n_sink = (it.s_end + kBK - 1) / kBK;
+                // the first product overwrites O_t once the previous item has been read out
+                if (i > 0) wait_bar(bar(B_OE + t), (uint32_t)(i - 1) & 1u, abort, c);
+                for (int k = 0; k < n_blk; ++k, ++g, r.next<kStages>()) {
+                    step<kBK>(b, k, n_sink, it);
+                    const uint32_t v_d = v_d0 + (uint32_t)(r.s * L::kTileK >> 4);
+                    wait_bar(bar(B_KF + r.s), r.phase, abort, c);
+                    if (b.kend - b.kv0 < b.nk) {
+                        arrive_if(one, bar(B_ZR));
+                        wait_bar(bar(B_VZ), nz & 1u, abort, c);
+                        ++nz;
+                    }
+                    wait_bar(bar(B_PF + t), g & 1u, abort, c);
+                    ptx::tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        umma_ts_if(kk * 16 < b.nk ? one : 0u, d_o, a_p + (uint32_t)(kk * 8), desc_at(v_d, kk * 2048), idesc,
+                                   (kk != 0 || k != 0) ? 1u : 0u);
+                    commit_if(one, bar(B_PV + t));
+                    commit_if(one, bar(B_KE + r.s));
+                }
+            }
+            commit_if(one, bar(B_DRAIN + 2 + t));
+            drain_bar(bar(B_DRAIN + 2 + t), 0, c);
+        } else if (warp == 5) {
             // ================= V rows past a block's keys =================
             // (asked by the issuers, which follow every block: this warp sees only
             // some, and a phase of the stage's own barrier could pass it by)
             uint32_t nz = 0;
-            for (uint32_t g = 0; wk.next(b); ++g) {
-                if (b.kend - b.kv0 >= b.nk) continue;
-                const int s = (int)(g % kStages);
-                const bool w = wait_bar(bar(B_ZR), nz++ & 1u, abort, c);
-                if (!__all_sync(0xffffffffu, w)) break;
-                zero_rows<D>(sm + L::V + s * L::kTileK, L::kBoxK, b.kend - b.kv0, b.nk, lane);
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(B_VZ));
-            }
-        } else {
-            // ================= MMA issuers: warp 1 for tile 0, warp 3 for tile 1 =================
-            if (lane == 0) {
-                const int t = warp == 1 ? 0 : 1;
-                const uint32_t d_s = tmem + L::S(t), a_p = tmem + L::P(t), d_o = tmem + L::O(t);
-                const uint32_t q_t = sQ + (uint32_t)(t * L::kTileQ);
-                // S_t = Q_t . K_g^T once the softmax has loaded S(g-1)
-                auto qk = [&](uint32_t g, const Blk &k) -> bool {
-                    const int s = (int)(g % kStages);
-                    if (!wait_bar(bar(B_KF + s), (g / kStages) & 1u, abort, c)) return false;
-                    if (g > 0 && !wait_bar(bar(B_SL + t), (g - 1u) & 1u, abort, c)) return false;
-                    ptx::tc_fence_after();
-                    const uint32_t idesc = ptx::idesc_16bit_f32(BF16, 128, k.nk, false);
-                    const uint32_t k_s = sK + (uint32_t)(s * L::kTileK);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        ptx::umma_bf16(d_s, kmajor_desc(q_t, kBoxQ, kk), kmajor_desc(k_s, L::kBoxK, kk), idesc, kk != 0 ? 1u : 0u);
-                    ptx::umma_commit(bar(B_SF + t));
-                    ptx::umma_commit(bar(B_KE + s));
-                    if (k.last) ptx::umma_commit(bar(B_QE));
-                    return true;
-                };
-                uint32_t nz = 0;  // zeroed blocks so far
-                // O_t (+)= P_t . V_g; an item's first product overwrites O_t once the
-                // previous item has been read out
-                auto pv = [&](uint32_t g, const Blk &k, uint32_t item) -> bool {
-                    const int s = (int)(g % kStages);
-                    if (!wait_bar(bar(B_VF + s), (g / kStages) & 1u, abort, c)) return false;
-                    if (k.kend - k.kv0 < k.nk) {
-                        ptx::mbar_arrive(bar(B_ZR));
-                        if (!wait_bar(bar(B_VZ), nz & 1u, abort, c)) return false;
-                        ++nz;
-                    }
-                    if (!wait_bar(bar(B_PF + t), g & 1u, abort, c)) return false;
-                    if (k.first && item > 0 && !wait_bar(bar(B_OE + t), (item - 1u) & 1u, abort, c)) return false;
-                    ptx::tc_fence_after();
-                    constexpr uint32_t idesc = ptx::idesc_16bit_f32(BF16, 128, D, true);
-                    for (int kk = 0; kk < k.nk / 16; ++kk)
-                        ptx::umma_bf16_ts(d_o, a_p + (uint32_t)(kk * 8),
-                                          mnmajor_desc(sV + (uint32_t)(s * L::kTileK), L::kBoxK, kk), idesc,
-                                          (kk != 0 || !k.first) ? 1u : 0u);
-                    ptx::umma_commit(bar(B_PV + t));
-                    ptx::umma_commit(bar(B_VE + s));
-                    return true;
-                };
-                Blk cur = {}, nxt = {};
-                bool ok = true, has = wk.next(cur);
-                uint32_t g = 0, ic = 0, item = 0;
-                if (has) {
-                    ok = wait_bar(bar(B_QF), 0u, abort, c);
-                    ic = 1;
-                    if (ok) ok = qk(0, cur);
+            for (int i = 0; i < n_items; ++i) {
+                const FwdItem &it = item_at(i);
+                const int n_blk = it.n_blk, n_sink = (it.s_end + kBK - 1) / kBK;
+                for (int k = 0; k < n_blk; ++k, r.next<kStages>()) {
+                    step<kBK>(b, k, n_sink, it);
+                    if (b.kend - b.kv0 >= b.nk) continue;
+                    wait_bar(bar(B_ZR), nz++ & 1u, abort, c);
+                    zero_rows<D>(sm + L::V + r.s * L::kTileK, L::kBoxK, b.kend - b.kv0, b.nk, lane);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    arrive_if(one, bar(B_VZ));
                 }
-                while (ok && has) {
-                    const bool has_next = wk.next(nxt);
-                    if (has_next && nxt.first) {
-                        if (!wait_bar(bar(B_QF), ic & 1u, abort, c)) break;
-                        ++ic;
-                    }
-                    if (has_next) ok = qk(g + 1u, nxt);
-                    if (ok) ok = pv(g, cur, item);
-                    if (!ok) break;
-                    if (has_next && nxt.first) ++item;
-                    cur = nxt;
-                    has = has_next;
-                    ++g;
-                }
-                // every MMA issued must complete before TMEM is released
-                ptx::umma_commit(bar(B_DRAIN + t));
-                drain_bar(bar(B_DRAIN + t), 0, c);
             }
         }
     } else {
         regs_inc();
         // ================= softmax of tile t, output rescaling, epilogue =================
-        const int t = (warp - 4) >> 2;
+        const int t = (warp - 8) >> 2;
         const int qd = warp & 3;
         const int row = qd * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
@@ -343,13 +326,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                 if (p.lse != nullptr) p.lse[r * c.H_q + it.head[t]] = -INFINITY;
             }
         }
+        __syncwarp();
         float mref = -INFINITY, lrow = 0.f;  // reference max (log2-scaled units), running sum
         const uint64_t scale2 = f2(c.scale_log2, c.scale_log2);
-        Walk<kBK> wk;
-        wk.init(p, items);
+        const int window = c.window, sinks = c.sinks;
+        int pos0 = 0;                        // position of the tile's first row
+        uint32_t g = 0;
         Blk b = {};
-        // one block: FULL, all kBK keys; else its first nk
-        auto block = [&](uint32_t g, auto full) -> bool {
+        // one block: FULL, all kBK keys, each seen by every row; else its first nk,
+        // masked (two bodies: the masks' selects would cost the first one registers
+        // and half of its time)
+        auto block = [&](bool first, auto full) {
             constexpr bool FULL = decltype(full)::value;
             uint32_t v[kBK];
 #pragma unroll
@@ -365,17 +352,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
             // the scores are in registers: the next block's may overwrite them
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(B_SL + t));
-            const int pos0 = wk.it->pos0[t], pos = pos0 + row;
-            // some row of the tile does not see every key of the block?
-            if (b.kv0 + kBK - 1 > pos0 || b.kend - b.kv0 < kBK ||
-                (b.kv0 <= pos0 + kBQ - 1 - c.window && b.kv0 + kBK > c.sinks)) {
+            arrive_if(one, bar(B_SL + t));
+            if constexpr (!FULL) {
+                const int pos = pos0 + row;
                 const int hi = clampi(min(b.kend, pos + 1) - b.kv0, 0, kBK);
-                const int lo = clampi(pos - c.window + 1 - b.kv0, 0, kBK);
-                const int sk = clampi(c.sinks - b.kv0, 0, kBK);
+                const int lo = clampi(pos - window + 1 - b.kv0, 0, kBK);
+                const int sk = clampi(sinks - b.kv0, 0, kBK);
+                uint32_t seen[(kBK + 31) / 32];
 #pragma unroll
-                for (int k = 0; k < kBK; ++k)
-                    if (k >= hi || (k < lo && k >= sk)) v[k] = __float_as_uint(-INFINITY);
+                for (int x = 0; x < (kBK + 31) / 32; ++x)
+                    seen[x] = bits_below(hi, 32 * x) & (~bits_below(lo, 32 * x) | bits_below(sk, 32 * x));
+                MaskRow<0, kBK>::apply(v, seen, __float_as_uint(-INFINITY));
             }
             // row max: eight interleaved partials, two new scores per three-input max
             float mp[8];
@@ -386,46 +373,61 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                 mp[(k >> 1) & 7] = max3(mp[(k >> 1) & 7], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
             const float mx = fmaxf(max3(mp[0], mp[1], mp[2]), fmaxf(max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7])));
             const float mcand = mx * c.scale_log2;
-            const bool need = !b.first && mcand > mref + kRescale;
+            const bool need = !first && mcand > mref + kRescale;
             const float alpha = need ? ex2(mref - mcand) : 1.f;
-            if (b.first || need) mref = mcand;
-            // P.V of the block before: its probabilities and the accumulator are ours
-            if (g > 0) {
-                const bool w = wait_bar(bar(B_PV + t), (g - 1u) & 1u, abort, c);
-                if (!__all_sync(0xffffffffu, w)) return false;
-                ptx::tc_fence_after();
-            }
-            if (__any_sync(0xffffffffu, need)) {
-#pragma unroll
-                for (int x = 0; x < D / 32; ++x) {
-                    uint32_t o[32];
-                    ptx::tmem_ld_32x32b_x32(to + (uint32_t)(x * 32), o);
-                    ptx::tmem_ld_wait();
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                    ptx::tmem_st_32x32b_x32(to + (uint32_t)(x * 32), o);
-                }
-            }
+            if (first || need) mref = mcand;
             const float base = mref == -INFINITY ? 0.f : mref;
             const uint64_t nbase2 = f2(-base, -base);
             uint64_t sp[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) sp[k] = f2(0.f, 0.f);
+            // first all exponentials, in place, then their sums and roundings: a pair
+            // that is used as soon as it is asked for costs the unit's whole latency
 #pragma unroll
             for (int x = 0; x < kBK / 16; ++x) {
                 if (FULL || x * 16 < b.nk) {
-                    uint32_t pk[8];
 #pragma unroll
-                    for (int k = 0; k < 16; k += 2) {
+                    for (int k = x * 16; k < x * 16 + 16; k += 2) {
                         float x0, x1;
-                        unf2(fma2(f2(__uint_as_float(v[x * 16 + k]), __uint_as_float(v[x * 16 + k + 1])), scale2, nbase2), x0, x1);
-                        const float p0 = ex2(x0), p1 = ex2(x1);
+                        unf2(fma2(f2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), scale2, nbase2), x0, x1);
+                        v[k] = __float_as_uint(ex2(x0));
+                        v[k + 1] = __float_as_uint(ex2(x1));
+                    }
+                }
+            }
+            uint32_t pk[kBK / 2];
+#pragma unroll
+            for (int x = 0; x < kBK / 16; ++x) {
+                if (FULL || x * 16 < b.nk) {
+#pragma unroll
+                    for (int k = x * 16; k < x * 16 + 16; k += 2) {
+                        const float p0 = __uint_as_float(v[k]), p1 = __uint_as_float(v[k + 1]);
                         sp[(k >> 1) & 3] = add2(sp[(k >> 1) & 3], f2(p0, p1));
                         pk[k >> 1] = pack16<BF16>(p0, p1);
                     }
-                    ptx::tmem_st_32x32b_x8(tp + (uint32_t)(x * 8), pk);
                 }
             }
+            // P.V of the block before, by now long under way: then its
+            // probabilities may be replaced and the accumulator rescaled
+            if (g > 0) {
+                wait_bar(bar(B_PV + t), (g - 1u) & 1u, abort, c);
+                ptx::tc_fence_after();
+            }
+            if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    uint32_t o[16];
+                    ptx::tmem_ld_32x32b_x16(to + (uint32_t)(x * 16), o);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                    ptx::tmem_st_32x32b_x8(to + (uint32_t)(x * 16), o);
+                    ptx::tmem_st_32x32b_x8(to + (uint32_t)(x * 16 + 8), o + 8);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < kBK / 16; ++x)
+                if (FULL || x * 16 < b.nk) ptx::tmem_st_32x32b_x8(tp + (uint32_t)(x * 8), pk + x * 8);
             float s0, s1, s2, s3;
             unf2(add2(sp[0], sp[1]), s0, s1);
             unf2(add2(sp[2], sp[3]), s2, s3);
@@ -433,36 +435,40 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(B_PF + t));
-            return true;
+            arrive_if(one, bar(B_PF + t));
         };
-        for (uint32_t g = 0; wk.next(b); ++g) {
-            if (b.first) {
-                mref = -INFINITY;
-                lrow = 0.f;
-            }
-            bool w = wait_bar(bar(B_SF + t), g & 1u, abort, c);
-            if (!__all_sync(0xffffffffu, w)) break;
-            ptx::tc_fence_after();
-            if (!(b.nk == kBK ? block(g, Bool<true>()) : block(g, Bool<false>()))) break;
-            if (b.last) {  // the item's output, after the tile's last P.V
-                w = wait_bar(bar(B_PV + t), g & 1u, abort, c);
-                if (!__all_sync(0xffffffffu, w)) break;
+        for (int i = 0; i < n_items; ++i) {
+            const FwdItem &it = item_at(i);
+            const int n_blk = it.n_blk, n_sink = (it.s_end + kBK - 1) / kBK;
+            mref = -INFINITY;
+            lrow = 0.f;
+            pos0 = it.pos0[t];
+            for (int k = 0; k < n_blk; ++k, ++g) {
+                step<kBK>(b, k, n_sink, it);
+                // every row of the tile sees every key of the block?
+                const bool full = b.kv0 + kBK - 1 <= pos0 && b.kend - b.kv0 >= kBK &&
+                                  (b.kv0 > pos0 + kBQ - 1 - window || b.kv0 + kBK <= sinks);
+                wait_bar(bar(B_SF + t), g & 1u, abort, c);
                 ptx::tc_fence_after();
-                // a row without a visible key: no sum, output 0, lse -inf
-                const bool none = lrow == 0.f;
-                const float inv = none ? 0.f : 1.f / lrow;
-                const int64_t r = wk.it->q_row[t] + row;
-                const int h = wk.it->head[t];
-                const bool mine = row < wk.it->n_rows[t];
-                uint16_t *dst = mine ? static_cast<uint16_t *>(p.o.p) + r * p.o.token + h * p.o.head : nullptr;
-                store_row<BF16, D>(dst, to, inv);
-                if (mine && p.lse != nullptr)  // natural log: (m + log2 l) * ln 2
-                    p.lse[r * c.H_q + h] = none ? -INFINITY : (mref + log2f(lrow)) * 0.69314718055994531f;
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(B_OE + t));
+                if (full) block(k == 0, Bool<true>());
+                else block(k == 0, Bool<false>());
             }
+            // the item's output, after the tile's last P.V
+            wait_bar(bar(B_PV + t), (g - 1u) & 1u, abort, c);
+            ptx::tc_fence_after();
+            // a row without a visible key: no sum, output 0, lse -inf
+            const bool none = lrow == 0.f;
+            const float inv = none ? 0.f : 1.f / lrow;
+            const int64_t r = it.q_row[t] + row;
+            const int h = it.head[t];
+            const bool mine = row < it.n_rows[t];
+            uint16_t *dst = mine ? static_cast<uint16_t *>(p.o.p) + r * p.o.token + h * p.o.head : nullptr;
+            store_row<BF16, D>(dst, to, inv);
+            if (mine && p.lse != nullptr)  // natural log: (m + log2 l) * ln 2
+                p.lse[r * c.H_q + h] = none ? -INFINITY : (mref + log2f(lrow)) * 0.69314718055994531f;
+            ptx::tc_fence_before();
+            __syncwarp();
+            arrive_if(one, bar(B_OE + t));
         }
     }
     ptx::tc_fence_before();
