@@ -16,10 +16,11 @@
 //   P, dS by the warpgroup g & 1        one stationary row per thread
 //   dV += P W (dK, dV form), dX += dS U  P and dS read from TMEM as 16-bit
 //
-//   warp 0      TMA producer: an item's X and Y, each block's U and W (ring)
-//   warp 1      MMA issuer: S, dP of block g, then the sums of block g - 1
-//   warp 2      zeroes streaming rows past the sequence's end
-//   warps 4-7, 8-11  the two warpgroups
+//   warp 0        TMA producer: an item's X and Y, each block's U and W (ring)
+//   warps 1, 2    issue S = X U^T and dP = Y W^T
+//   warps 3, 4    issue dX += dS U and (dK, dV form) dY += P W
+//   warp 5        zeroes streaming rows past the sequence's end
+//   warps 8-11, 12-15  the two warpgroups
 //
 // TMEM (512 columns): buffer b: S at 128b, dP at 128b + 64 (P and dS over
 // their first 32 columns); sums at 256 and 384.  The dQ form has one sum and
@@ -34,23 +35,23 @@ namespace {
 
 constexpr int kBX = 128, kBU = 64;
 constexpr int kBoxX = kBX * 128, kBoxU = kBU * 128;
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kStages = 4;
 
 enum {
     B_XF = 0,                  // the item's X, Y landed
-    B_XE = 1,                  // X, Y read by the item's last S, dP
+    B_XE = 1,                  // X, Y read by the item's last S, dP (a commit of each issuer)
     B_UF = 2,                  // stage landed
-    B_UE = B_UF + kStages,     // stage consumed
-    B_ZR = B_UE + kStages,     // a block with rows past the end landed
+    B_UE = B_UF + kStages,     // stage consumed (a commit of each sum's issuer)
+    B_ZR = B_UE + kStages,     // a block with rows past the end landed (asked by both S, dP issuers)
     B_UZ = B_ZR + 1,           // its rows past the end zeroed
-    B_SF = B_UZ + 1,           // buffer b: S, dP written (2)
+    B_SF = B_UZ + 1,           // buffer b: S, dP written (2; a commit of each issuer)
     B_PF = B_SF + 2,           // buffer b: P, dS written (2)
-    B_DN = B_PF + 2,           // buffer b: sums updated (2)
-    B_AF = B_DN + 2,           // an item's sums complete
+    B_DN = B_PF + 2,           // buffer b: sums updated (2; a commit of each sum's issuer)
+    B_AF = B_DN + 2,           // an item's sums complete (a commit of each sum's issuer)
     B_OE = B_AF + 1,           // sum place read out (2)
-    B_DRAIN = B_OE + 2,
-    N_BAR = B_DRAIN + 1
+    B_DRAIN = B_OE + 2,        // every MMA of an issuer completed (4)
+    N_BAR = B_DRAIN + 4
 };
 
 template <int D> struct Lay {
@@ -117,8 +118,10 @@ template <bool KEYS> struct Walk {
     }
 };
 
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 96;"); }
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 200;"); }
+// The first eight warps keep 72 of the 128 registers launched, the two
+// warpgroups take 184: 256 * 72 + 256 * 184 = 65,536.
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 184;"); }
 
 // Probabilities and score gradients of columns 2K, 2K + 1 ..: 0 where not seen
 template <int K> struct PairRow {
@@ -171,7 +174,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
         *abort = 0;
         for (int i = 0; i < N_BAR; ++i) {
             const bool four = i >= B_PF && i < B_PF + 2, eight = i >= B_OE && i < B_OE + 2;
-            ptx::mbar_init(bar(i), four ? 4 : eight ? 8 : 1);
+            const bool products = i == B_XE || i == B_ZR || i == B_SF || i == B_SF + 1;
+            const bool sums = i == B_DN || i == B_DN + 1 || i == B_AF || (i >= B_UE && i < B_UE + kStages);
+            ptx::mbar_init(bar(i), four ? 4 : eight ? 8 : products || (sums && KEYS) ? 2 : 1);
         }
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
@@ -185,7 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp < 4) {
+    const uint32_t one = lane == 0 ? 1u : 0u;
+    if (warp < 8) {
         regs_dec();
         Walk<KEYS> wk;
         wk.init(p);
@@ -228,9 +234,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
             if (ic > 0) drain_bar(bar(B_XF), (ic - 1u) & 1u, c);
             for (uint32_t s = 0; s < kStages; ++s)
                 if (g > s) drain_bar(bar(B_UF + (int)s), ((g - 1u - s) / kStages) & 1u, c);
-        } else if (warp == 2) {
+        } else if (warp == 5) {
             // ================= streaming rows past the end =================
-            // (asked by the issuer, which follows every block: this warp sees only
+            // (asked by the issuers, which follow every block: this warp sees only
             // some, and a phase of the stage's own barrier could pass it by)
             uint32_t nz = 0;
             for (uint32_t g = 0; wk.next(p, b); ++g) {
@@ -241,79 +247,72 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
                 zero_rows<D>(sm + L::RING + s * L::kStage + L::kTileU, kBoxU, b.valid, kBU, lane);
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(B_UZ));
+                arrive_if(one, bar(B_UZ));
             }
-        } else if (warp == 1) {
-            // ================= MMA issuer =================
+        } else if (warp <= 2) {
+            // ================= S = X U^T (warp 1), dP = Y W^T (warp 2) =================
+            const bool is_dp = warp == 2;
             constexpr uint32_t id_s = ptx::idesc_16bit_f32(BF16, 128, kBU, false);
-            constexpr uint32_t id_a = ptx::idesc_16bit_f32(BF16, 128, D, true);
-            const uint32_t x_d = desc_lo(sbase + L::X, 16), y_d = desc_lo(sbase + L::Y, 16);
-            const uint32_t u_k = desc_lo(sbase + L::RING, 16), u_m = desc_lo(sbase + L::RING, kBoxU);
-            uint32_t nz = 0, ic = 0;
-            // sums of block g: dX (+)= dS U, and dY (+)= P W in the dK, dV form
-            auto sums = [&](uint32_t g, const Blk &k, uint32_t item) {
-                const int s = (int)(g % kStages);
-                const uint32_t buf = tmem + (g & 1u) * 128u;
-                if (k.first) {  // the place's previous output has been read
-                    if (KEYS && item > 0) wait_bar(bar(B_OE), (item - 1u) & 1u, abort, c);
-                    if (!KEYS && item > 1) wait_bar(bar(B_OE + (int)(item & 1u)), ((item >> 1) - 1u) & 1u, abort, c);
-                }
-                wait_bar(bar(B_PF + (int)(g & 1u)), (g >> 1) & 1u, abort, c);
-                ptx::tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t u = u_m + (uint32_t)(s * L::kStage >> 4);
-                    const uint32_t dx = tmem + 256u + (KEYS ? 0u : (item & 1u) * 128u);
-#pragma unroll
-                    for (int kk = 0; kk < kBU / 16; ++kk) {
-                        const uint32_t acc = (kk != 0 || !k.first) ? 1u : 0u;
-                        if (KEYS) ptx::umma_bf16_ts(tmem + 384u, buf + (uint32_t)(kk * 8), desc_at(u, L::kTileU + kk * 2048), id_a, acc);
-                        ptx::umma_bf16_ts(dx, buf + 64u + (uint32_t)(kk * 8), desc_at(u, kk * 2048), id_a, acc);
-                    }
-                    ptx::umma_commit(bar(B_DN + (int)(g & 1u)));
-                    ptx::umma_commit(bar(B_UE + s));
-                    if (k.last) ptx::umma_commit(bar(B_AF));
-                }
-                __syncwarp();
-            };
-            Blk prev = {};
-            uint32_t g = 0;
+            const uint32_t x_d = desc_lo(sbase + (is_dp ? L::Y : L::X), 16);
+            const uint32_t u_d = desc_lo(sbase + L::RING + (is_dp ? L::kTileU : 0), 16);
+            uint32_t g = 0, ic = 0, nz = 0;
             for (; wk.next(p, b); ++g) {
-                if (b.first) wait_bar(bar(B_XF), ic++ & 1u, abort, c);
                 const int s = (int)(g % kStages);
+                if (b.first) wait_bar(bar(B_XF), ic++ & 1u, abort, c);
                 wait_bar(bar(B_UF + s), (g / kStages) & 1u, abort, c);
                 if (b.valid < kBU) {
-                    if (lane == 0) ptx::mbar_arrive(bar(B_ZR));
+                    arrive_if(one, bar(B_ZR));
                     wait_bar(bar(B_UZ), nz++ & 1u, abort, c);
                 }
                 // buffer g & 1: P, dS of block g - 2 read
                 if (g > 1) wait_bar(bar(B_DN + (int)(g & 1u)), ((g >> 1) - 1u) & 1u, abort, c);
                 ptx::tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t u = u_k + (uint32_t)(s * L::kStage >> 4);
-                    const uint32_t buf = tmem + (g & 1u) * 128u;
+                const uint32_t u = u_d + (uint32_t)(s * L::kStage >> 4), dst = tmem + (g & 1u) * 128u + (is_dp ? 64u : 0u);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const int ox = (kk >> 2) * kBoxX + (kk & 3) * 32, ou = (kk >> 2) * kBoxU + (kk & 3) * 32;
-                        ptx::umma_bf16(buf, desc_at(x_d, ox), desc_at(u, ou), id_s, kk != 0 ? 1u : 0u);
-                        ptx::umma_bf16(buf + 64u, desc_at(y_d, ox), desc_at(u, L::kTileU + ou), id_s, kk != 0 ? 1u : 0u);
-                    }
-                    ptx::umma_commit(bar(B_SF + (int)(g & 1u)));
-                    if (b.last) ptx::umma_commit(bar(B_XE));
-                }
-                __syncwarp();
-                if (g > 0) sums(g - 1u, prev, b.first ? ic - 2u : ic - 1u);
-                prev = b;
+                for (int kk = 0; kk < D / 16; ++kk)
+                    umma_if(one, dst, desc_at(x_d, (kk >> 2) * kBoxX + (kk & 3) * 32), desc_at(u, (kk >> 2) * kBoxU + (kk & 3) * 32),
+                            id_s, kk != 0 ? 1u : 0u);
+                commit_if(one, bar(B_SF + (int)(g & 1u)));
+                if (b.last) commit_if(one, bar(B_XE));
             }
-            if (g > 0) sums(g - 1u, prev, ic - 1u);
             // every MMA issued must complete before TMEM is released
-            if (lane == 0) ptx::umma_commit(bar(B_DRAIN));
-            __syncwarp();
-            drain_bar(bar(B_DRAIN), 0, c);
+            commit_if(one, bar(B_DRAIN + warp - 1));
+            drain_bar(bar(B_DRAIN + warp - 1), 0, c);
+        } else if (warp == 3 || (KEYS && warp == 4)) {
+            // ================= dX += dS U (warp 3), dY += P W (warp 4) =================
+            const bool is_y = warp == 4;
+            constexpr uint32_t id_a = ptx::idesc_16bit_f32(BF16, 128, D, true);
+            const uint32_t u_d = desc_lo(sbase + L::RING + (is_y ? L::kTileU : 0), kBoxU);
+            uint32_t g = 0, item = 0;
+            for (; wk.next(p, b); ++g) {
+                const int s = (int)(g % kStages);
+                if (b.first) {  // the place's previous output has been read
+                    if (KEYS && item > 0) wait_bar(bar(B_OE), (item - 1u) & 1u, abort, c);
+                    if (!KEYS && item > 1) wait_bar(bar(B_OE + (int)(item & 1u)), ((item >> 1) - 1u) & 1u, abort, c);
+                }
+                const uint32_t u = u_d + (uint32_t)(s * L::kStage >> 4);
+                const uint32_t src = tmem + (g & 1u) * 128u + (is_y ? 0u : 64u);
+                const uint32_t dst = tmem + 256u + (is_y ? 128u : KEYS ? 0u : (item & 1u) * 128u);
+                wait_bar(bar(B_UF + s), (g / kStages) & 1u, abort, c);
+                wait_bar(bar(B_PF + (int)(g & 1u)), (g >> 1) & 1u, abort, c);
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < kBU / 16; ++kk)
+                    umma_ts_if(one, dst, src + (uint32_t)(kk * 8), desc_at(u, kk * 2048), id_a, (kk != 0 || !b.first) ? 1u : 0u);
+                commit_if(one, bar(B_DN + (int)(g & 1u)));
+                commit_if(one, bar(B_UE + s));
+                if (b.last) {
+                    commit_if(one, bar(B_AF));
+                    ++item;
+                }
+            }
+            commit_if(one, bar(B_DRAIN + warp - 1));
+            drain_bar(bar(B_DRAIN + warp - 1), 0, c);
         }
     } else {
         regs_inc();
         // ================= P and dS of the warpgroup's blocks; the items' outputs =================
-        const int wg = (warp - 4) >> 2;
+        const int wg = (warp - 8) >> 2;
         const int qd = warp & 3;
         const int row = qd * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
@@ -395,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(B_PF + wg));
+                arrive_if(one, bar(B_PF + wg));
             }
             if (b.last) {  // the item's sums are complete
                 wait_bar(bar(B_AF), item & 1u, abort, c);
@@ -421,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(B_OE + (KEYS ? 0 : (int)(item & 1u))));
+                arrive_if(one, bar(B_OE + (KEYS ? 0 : (int)(item & 1u))));
                 ++item;
             }
         }
