@@ -12,7 +12,7 @@
 // head each way.  With X, Y the stationary tiles (K, V or Q, dO) and U, W the
 // streaming ones (Q, dO or K, V), a 64-row block does
 //
-//   S = X U^T, dP = Y W^T               128 x 64 each, into TMEM buffer g & 1
+//   S = X U^T, dP = Y W^T               128 x 64 each, into TMEM
 //   P, dS by the warpgroup g & 1        one stationary row per thread
 //   dV += P W (dK, dV form), dX += dS U  P and dS read from TMEM as 16-bit
 //
@@ -22,10 +22,11 @@
 //   warp 5        zeroes streaming rows past the sequence's end
 //   warps 8-11, 12-15  the two warpgroups
 //
-// TMEM (512 columns): buffer b: S at 128b, dP at 128b + 64 (P and dS over
-// their first 32 columns); sums at 256 and 384.  The dQ form has one sum and
-// alternates between the two places, so an item's output is read while the
-// next item's products run.
+// TMEM (512 columns): three places of 64 for S, over which the block's P and dS
+// (32 each) stay until their sums are made; one place for dP, free again as
+// soon as the warpgroup has loaded it; sums at 256 and 384.  So three blocks are
+// under way at a time.  The dQ form has one sum and alternates between the two
+// places, so an item's output is read while the next item's products run.
 #include "window.cuh"
 
 namespace syn {
@@ -45,10 +46,11 @@ enum {
     B_UE = B_UF + kStages,     // stage consumed (a commit of each sum's issuer)
     B_ZR = B_UE + kStages,     // a block with rows past the end landed (asked by both S, dP issuers)
     B_UZ = B_ZR + 1,           // its rows past the end zeroed
-    B_SF = B_UZ + 1,           // buffer b: S, dP written (2; a commit of each issuer)
-    B_PF = B_SF + 2,           // buffer b: P, dS written (2)
-    B_DN = B_PF + 2,           // buffer b: sums updated (2; a commit of each sum's issuer)
-    B_AF = B_DN + 2,           // an item's sums complete (a commit of each sum's issuer)
+    B_SF = B_UZ + 1,           // S and dP of block g written (6, g % 6; a commit of each issuer)
+    B_TL = B_SF + 6,           // dP of block g loaded into registers
+    B_PF = B_TL + 1,           // P, dS of block g written (3, g % 3)
+    B_DN = B_PF + 3,           // sums updated by block g (3, g % 3; a commit of each sum's issuer)
+    B_AF = B_DN + 3,           // an item's sums complete (a commit of each sum's issuer)
     B_OE = B_AF + 1,           // sum place read out (2)
     B_DRAIN = B_OE + 2,        // every MMA of an issuer completed (4)
     N_BAR = B_DRAIN + 4
@@ -173,9 +175,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
     if (threadIdx.x == 0) {
         *abort = 0;
         for (int i = 0; i < N_BAR; ++i) {
-            const bool four = i >= B_PF && i < B_PF + 2, eight = i >= B_OE && i < B_OE + 2;
-            const bool products = i == B_XE || i == B_ZR || i == B_SF || i == B_SF + 1;
-            const bool sums = i == B_DN || i == B_DN + 1 || i == B_AF || (i >= B_UE && i < B_UE + kStages);
+            const bool four = i == B_TL || (i >= B_PF && i < B_PF + 3), eight = i >= B_OE && i < B_OE + 2;
+            const bool products = i == B_XE || i == B_ZR || (i >= B_SF && i < B_SF + 6);
+            const bool sums = (i >= B_DN && i < B_DN + 3) || i == B_AF || (i >= B_UE && i < B_UE + kStages);
             ptx::mbar_init(bar(i), four ? 4 : eight ? 8 : products || (sums && KEYS) ? 2 : 1);
         }
         ptx::fence_mbar_init();
@@ -264,15 +266,19 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
                     arrive_if(one, bar(B_ZR));
                     wait_bar(bar(B_UZ), nz++ & 1u, abort, c);
                 }
-                // buffer g & 1: P, dS of block g - 2 read
-                if (g > 1) wait_bar(bar(B_DN + (int)(g & 1u)), ((g >> 1) - 1u) & 1u, abort, c);
+                // S: the sums of block g - 3 have read P and dS; dP: block g - 1's is loaded
+                if (is_dp) {
+                    if (g > 0) wait_bar(bar(B_TL), (g - 1u) & 1u, abort, c);
+                } else if (g > 2) {
+                    wait_bar(bar(B_DN + (int)(g % 3u)), (g / 3u - 1u) & 1u, abort, c);
+                }
                 ptx::tc_fence_after();
-                const uint32_t u = u_d + (uint32_t)(s * L::kStage >> 4), dst = tmem + (g & 1u) * 128u + (is_dp ? 64u : 0u);
+                const uint32_t u = u_d + (uint32_t)(s * L::kStage >> 4), dst = tmem + (is_dp ? 192u : (g % 3u) * 64u);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     umma_if(one, dst, desc_at(x_d, (kk >> 2) * kBoxX + (kk & 3) * 32), desc_at(u, (kk >> 2) * kBoxU + (kk & 3) * 32),
                             id_s, kk != 0 ? 1u : 0u);
-                commit_if(one, bar(B_SF + (int)(g & 1u)));
+                commit_if(one, bar(B_SF + (int)(g % 6u)));
                 if (b.last) commit_if(one, bar(B_XE));
             }
             // every MMA issued must complete before TMEM is released
@@ -291,15 +297,15 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
                     if (!KEYS && item > 1) wait_bar(bar(B_OE + (int)(item & 1u)), ((item >> 1) - 1u) & 1u, abort, c);
                 }
                 const uint32_t u = u_d + (uint32_t)(s * L::kStage >> 4);
-                const uint32_t src = tmem + (g & 1u) * 128u + (is_y ? 0u : 64u);
+                const uint32_t src = tmem + (g % 3u) * 64u + (is_y ? 0u : 32u);  // P, dS
                 const uint32_t dst = tmem + 256u + (is_y ? 128u : KEYS ? 0u : (item & 1u) * 128u);
                 wait_bar(bar(B_UF + s), (g / kStages) & 1u, abort, c);
-                wait_bar(bar(B_PF + (int)(g & 1u)), (g >> 1) & 1u, abort, c);
+                wait_bar(bar(B_PF + (int)(g % 3u)), (g / 3u) & 1u, abort, c);
                 ptx::tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < kBU / 16; ++kk)
                     umma_ts_if(one, dst, src + (uint32_t)(kk * 8), desc_at(u, kk * 2048), id_a, (kk != 0 || !b.first) ? 1u : 0u);
-                commit_if(one, bar(B_DN + (int)(g & 1u)));
+                commit_if(one, bar(B_DN + (int)(g % 3u)));
                 commit_if(one, bar(B_UE + s));
                 if (b.last) {
                     commit_if(one, bar(B_AF));
@@ -316,7 +322,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
         const int qd = warp & 3;
         const int row = qd * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
-        const uint32_t ts = tl + (uint32_t)(wg * 128);
         const uint64_t scale2 = f2(c.scale_log2, c.scale_log2);
         Walk<KEYS> wk;
         wk.init(p);
@@ -333,16 +338,21 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
             }
             if ((g & 1u) == (uint32_t)wg) {
                 const int s = (int)(g % kStages);
-                wait_bar(bar(B_SF + wg), (g >> 1) & 1u, abort, c);
+                wait_bar(bar(B_SF + (int)(g % 6u)), (g / 6u) & 1u, abort, c);
+                const uint32_t ts = tl + (g % 3u) * 64u;
                 if (KEYS) wait_bar(bar(B_UF + s), (g / kStages) & 1u, abort, c);  // the statistics
                 ptx::tc_fence_after();
                 uint32_t sv[64], dv[64];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     ptx::tmem_ld_32x32b_x32(ts + (uint32_t)(x * 32), *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * x));
-                    ptx::tmem_ld_32x32b_x32(ts + 64u + (uint32_t)(x * 32), *reinterpret_cast<uint32_t(*)[32]>(dv + 32 * x));
+                    ptx::tmem_ld_32x32b_x32(tl + 192u + (uint32_t)(x * 32), *reinterpret_cast<uint32_t(*)[32]>(dv + 32 * x));
                 }
                 ptx::tmem_ld_wait();
+                // (the next block's dP may take its place)
+                ptx::tc_fence_before();
+                __syncwarp();
+                arrive_if(one, bar(B_TL));
                 // columns [lo, hi) and those below sk are seen
                 const int pos = it.pos0 + row;
                 int lo, hi, sk = 0;
@@ -390,11 +400,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
                     PairRow<0>::apply(pk, dk, seen);
                 }
                 if (KEYS) ptx::tmem_st_32x32b_x32(ts, pk);
-                ptx::tmem_st_32x32b_x32(ts + 64u, dk);
+                ptx::tmem_st_32x32b_x32(ts + 32u, dk);
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
                 __syncwarp();
-                arrive_if(one, bar(B_PF + wg));
+                arrive_if(one, bar(B_PF + (int)(g % 3u)));
             }
             if (b.last) {  // the item's sums are complete
                 wait_bar(bar(B_AF), item & 1u, abort, c);

@@ -136,8 +136,8 @@ template <bool BF16, int D> __device__ __forceinline__ void store_row(void *dst_
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 184;"); }
 
-template <bool B> struct Bool {
-    static constexpr bool value = B;
+template <int V> struct Int {
+    static constexpr int value = V;
 };
 
 template <int D, bool BF16>
@@ -333,43 +333,37 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
         int pos0 = 0;                        // position of the tile's first row
         uint32_t g = 0;
         Blk b = {};
-        // one block: FULL, all kBK keys, each seen by every row; else its first nk,
-        // masked (two bodies: the masks' selects would cost the first one registers
-        // and half of its time)
-        auto block = [&](bool first, auto full) {
-            constexpr bool FULL = decltype(full)::value;
-            uint32_t v[kBK];
+        // one block of N score columns (kBK, or 16 where that covers its keys): with
+        // MASK, those that the row sees (columns past nk are stale, and masked).  A
+        // body of its own without the masks, whose selects take as long as the rest.
+        auto block = [&](bool first, auto cols, auto masked) {
+            constexpr int N = decltype(cols)::value;
+            constexpr bool MASK = decltype(masked)::value;
+            uint32_t v[N];
 #pragma unroll
-            for (int x = 0; x < kBK / 16; ++x) {
-                if (FULL || x * 16 < b.nk) {
-                    ptx::tmem_ld_32x32b_x16(ts + (uint32_t)(x * 16), v + 16 * x);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) v[x * 16 + k] = __float_as_uint(-INFINITY);
-                }
-            }
+            for (int x = 0; x < N / 16; ++x) ptx::tmem_ld_32x32b_x16(ts + (uint32_t)(x * 16), v + 16 * x);
             ptx::tmem_ld_wait();
             // the scores are in registers: the next block's may overwrite them
             ptx::tc_fence_before();
             __syncwarp();
             arrive_if(one, bar(B_SL + t));
-            if constexpr (!FULL) {
+            if constexpr (MASK) {
                 const int pos = pos0 + row;
                 const int hi = clampi(min(b.kend, pos + 1) - b.kv0, 0, kBK);
                 const int lo = clampi(pos - window + 1 - b.kv0, 0, kBK);
                 const int sk = clampi(sinks - b.kv0, 0, kBK);
-                uint32_t seen[(kBK + 31) / 32];
+                uint32_t seen[(N + 31) / 32];
 #pragma unroll
-                for (int x = 0; x < (kBK + 31) / 32; ++x)
+                for (int x = 0; x < (N + 31) / 32; ++x)
                     seen[x] = bits_below(hi, 32 * x) & (~bits_below(lo, 32 * x) | bits_below(sk, 32 * x));
-                MaskRow<0, kBK>::apply(v, seen, __float_as_uint(-INFINITY));
+                MaskRow<0, N>::apply(v, seen, __float_as_uint(-INFINITY));
             }
             // row max: eight interleaved partials, two new scores per three-input max
             float mp[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) mp[k] = __uint_as_float(v[k]);
 #pragma unroll
-            for (int k = 8; k < kBK; k += 2)
+            for (int k = 8; k < N; k += 2)
                 mp[(k >> 1) & 7] = max3(mp[(k >> 1) & 7], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
             const float mx = fmaxf(max3(mp[0], mp[1], mp[2]), fmaxf(max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7])));
             const float mcand = mx * c.scale_log2;
@@ -381,31 +375,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
             uint64_t sp[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) sp[k] = f2(0.f, 0.f);
-            // first all exponentials, in place, then their sums and roundings: a pair
-            // that is used as soon as it is asked for costs the unit's whole latency
+            uint32_t pk[N / 2];
 #pragma unroll
-            for (int x = 0; x < kBK / 16; ++x) {
-                if (FULL || x * 16 < b.nk) {
-#pragma unroll
-                    for (int k = x * 16; k < x * 16 + 16; k += 2) {
-                        float x0, x1;
-                        unf2(fma2(f2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), scale2, nbase2), x0, x1);
-                        v[k] = __float_as_uint(ex2(x0));
-                        v[k + 1] = __float_as_uint(ex2(x1));
-                    }
-                }
-            }
-            uint32_t pk[kBK / 2];
-#pragma unroll
-            for (int x = 0; x < kBK / 16; ++x) {
-                if (FULL || x * 16 < b.nk) {
-#pragma unroll
-                    for (int k = x * 16; k < x * 16 + 16; k += 2) {
-                        const float p0 = __uint_as_float(v[k]), p1 = __uint_as_float(v[k + 1]);
-                        sp[(k >> 1) & 3] = add2(sp[(k >> 1) & 3], f2(p0, p1));
-                        pk[k >> 1] = pack16<BF16>(p0, p1);
-                    }
-                }
+            for (int k = 0; k < N; k += 2) {
+                float x0, x1;
+                unf2(fma2(f2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), scale2, nbase2), x0, x1);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                sp[(k >> 1) & 3] = add2(sp[(k >> 1) & 3], f2(p0, p1));
+                pk[k >> 1] = pack16<BF16>(p0, p1);
             }
             // P.V of the block before, by now long under way: then its
             // probabilities may be replaced and the accumulator rescaled
@@ -426,8 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                 }
             }
 #pragma unroll
-            for (int x = 0; x < kBK / 16; ++x)
-                if (FULL || x * 16 < b.nk) ptx::tmem_st_32x32b_x8(tp + (uint32_t)(x * 8), pk + x * 8);
+            for (int x = 0; x < N / 16; ++x) ptx::tmem_st_32x32b_x8(tp + (uint32_t)(x * 8), pk + x * 8);
             float s0, s1, s2, s3;
             unf2(add2(sp[0], sp[1]), s0, s1);
             unf2(add2(sp[2], sp[3]), s2, s3);
@@ -450,8 +426,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                                   (b.kv0 > pos0 + kBQ - 1 - window || b.kv0 + kBK <= sinks);
                 wait_bar(bar(B_SF + t), g & 1u, abort, c);
                 ptx::tc_fence_after();
-                if (full) block(k == 0, Bool<true>());
-                else block(k == 0, Bool<false>());
+                if (full) block(k == 0, Int<kBK>(), Int<0>());
+                else if (b.nk > 16) block(k == 0, Int<kBK>(), Int<1>());
+                else block(k == 0, Int<16>(), Int<1>());
             }
             // the item's output, after the tile's last P.V
             wait_bar(bar(B_PV + t), (g - 1u) & 1u, abort, c);
