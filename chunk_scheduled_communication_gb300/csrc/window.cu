@@ -1,5 +1,5 @@
 // window.cu -- plans and C ABI of the windowed attention over ragged sequences
-// (include/syn_window.h; kernels in window_fwd.cu and window_bwd.cu).
+// (include/syn_window.h; kernels in window_fwd.cu, window_dkv.cu and window_dq.cu).
 //
 // A plan turns the sequences' lengths into work items and deals them out to
 // one persistent CTA per SM: the largest first, each to the CTA with the least
@@ -149,11 +149,13 @@ void build_forward(Lists &l, const syn_window_cfg_t &c, int64_t window, int64_t 
             }
 }
 
+int64_t pad_to_block(int64_t rows) { return (rows + 63) / 64 * 64; }
+
 void build_queries(Lists &l, const syn_window_cfg_t &c, int64_t window, int64_t q0, int64_t k0, int64_t ql, int64_t kl) {
     const int G = c.H_q / c.H_kv;
     const int64_t off = kl - ql;
-    for (int64_t i0 = 0; i0 < ql; i0 += 64)
-        l.prep.push_back({(int32_t)(q0 + i0), (int32_t)std::min<int64_t>(64, ql - i0), (int32_t)(l.pad_rows + i0), 0});
+    for (int64_t i0 = 0; i0 < pad_to_block(ql); i0 += 64)
+        l.prep.push_back({(int32_t)(q0 + i0), (int32_t)std::max<int64_t>(0, std::min<int64_t>(64, ql - i0)), (int32_t)(l.pad_rows + i0), 0});
     for (int hk = 0; hk < c.H_kv; ++hk)
         for (int64_t i0 = 0; i0 < ql; i0 += 128)
             for (int h = hk * G; h < (hk + 1) * G; ++h) {
@@ -172,7 +174,7 @@ void build_queries(Lists &l, const syn_window_cfg_t &c, int64_t window, int64_t 
                 it.part = -1;
                 if (off + last >= 0) key_ranges(off + i0, off + last, window, c.sinks, it.s_end, it.w_lo, it.k_end);
                 l.queries.push_back(it);
-                l.query_cost.push_back(ceil_div(it.s_end, 64) + ceil_div(it.k_end - it.w_lo, 64) + 3);
+                l.query_cost.push_back(ceil_div(it.s_end, 128) + ceil_div(it.k_end - it.w_lo, 128) + 1);
             }
 }
 
@@ -342,7 +344,10 @@ int syn_window_plan_create(syn_window_plan_t *out, const syn_window_cfg_t *cfg, 
     PL_CK(cudaGetDevice(&pl->device));
     PL_CK(cudaDeviceGetAttribute(&pl->num_sms, cudaDevAttrMultiProcessorCount, pl->device));
     PL_CK(fwd_prepare(c.d, pl->bf16));
-    if (c.backward) PL_CK(bwd_prepare(c.d, pl->bf16));
+    if (c.backward) {
+        PL_CK(dkv_prepare(c.d, pl->bf16));
+        PL_CK(dq_prepare(c.d, pl->bf16));
+    }
 
     // parts of at most `most` blocks: a third of what one CTA gets in all
     const int G = c.H_q / c.H_kv;
@@ -362,7 +367,7 @@ int syn_window_plan_create(syn_window_plan_t *out, const syn_window_cfg_t *cfg, 
         if (c.backward) {
             build_queries(l, c, c.window, q0, k0, ql, kl);
             build_keys(l, c, c.window, q0, k0, ql, kl, most);
-            l.pad_rows += (ql + 63) / 64 * 64;
+            l.pad_rows += pad_to_block(ql);
         }
         pairs += count_pairs(ql, kl, c.window, c.sinks);
         q0 += ql;
@@ -509,20 +514,20 @@ int syn_window_attention_backward(syn_window_plan_t pl, const syn_window_rows_t 
         if ((rc = encode(&keys.x, pl, *K, nk, c.H_kv, 128)) != SYN_OK || (rc = encode(&keys.y, pl, *V, nk, c.H_kv, 128)) != SYN_OK ||
             (rc = encode(&keys.u, pl, *Q, nq, c.H_q, 64)) != SYN_OK || (rc = encode(&keys.w, pl, *dO, nq, c.H_q, 64)) != SYN_OK ||
             (rc = encode(&queries.x, pl, *Q, nq, c.H_q, 128)) != SYN_OK || (rc = encode(&queries.y, pl, *dO, nq, c.H_q, 128)) != SYN_OK ||
-            (rc = encode(&queries.u, pl, *K, nk, c.H_kv, 64)) != SYN_OK || (rc = encode(&queries.w, pl, *V, nk, c.H_kv, 64)) != SYN_OK)
+            (rc = encode(&queries.u, pl, *K, nk, c.H_kv, 128)) != SYN_OK || (rc = encode(&queries.w, pl, *V, nk, c.H_kv, 128)) != SYN_OK)
             return rc;
         if (pl->grid_k > 0) {
             p.items = pl->d_key_items;
             p.begin = pl->d_key_begin;
             p.dx = out_of(dK);
             p.dy = out_of(dV);
-            WIN_CK(bwd_launch(c.d, pl->bf16, true, pl->grid_k, p, keys, st));
+            WIN_CK(dkv_launch(c.d, pl->bf16, pl->grid_k, p, keys, st));
         }
         if (pl->grid_q > 0) {
             p.items = pl->d_query_items;
             p.begin = pl->d_query_begin;
             p.dx = out_of(dQ);
-            WIN_CK(bwd_launch(c.d, pl->bf16, false, pl->grid_q, p, queries, st));
+            WIN_CK(dq_launch(c.d, pl->bf16, pl->grid_q, p, queries, st));
         }
     } else if (nq > 0) {  // no key at all: dQ = 0
         for (int h = 0; h < c.H_q; ++h)

@@ -27,8 +27,7 @@ struct alignas(16) FwdItem {
     int32_t kv_row0, hk, s_end, w_lo, k_end, n_blk, pad[2];
 };
 
-// Gradient work item of either kernel: 128 stationary rows and the 64-row
-// blocks that stream past them.
+// Gradient work item: 128 stationary rows, and what streams past them.
 //   dK, dV: stationary keys j0 .. of kv head hk; query blocks [b0, b1) of 64
 //           rows of the sequence for each head of [h0, h1)
 //   dQ:     stationary query rows of head h0; key blocks of the sinks
@@ -263,6 +262,29 @@ template <int D> __device__ __forceinline__ void zero_rows(uint8_t *tile, int bo
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
 
+// 32 accumulator columns of this thread's row to 16-bit (dst) or fp32 (part)
+template <bool BF16>
+__device__ __forceinline__ void store_cols(uint32_t taddr, uint16_t *dst, float *part, float scale) {
+    uint32_t v[32];
+    ptx::tmem_ld_32x32b_x32(taddr, v);
+    ptx::tmem_ld_wait();
+    if (dst != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint4 o;
+            o.x = pack16<BF16>(__uint_as_float(v[8 * k + 0]) * scale, __uint_as_float(v[8 * k + 1]) * scale);
+            o.y = pack16<BF16>(__uint_as_float(v[8 * k + 2]) * scale, __uint_as_float(v[8 * k + 3]) * scale);
+            o.z = pack16<BF16>(__uint_as_float(v[8 * k + 4]) * scale, __uint_as_float(v[8 * k + 5]) * scale);
+            o.w = pack16<BF16>(__uint_as_float(v[8 * k + 6]) * scale, __uint_as_float(v[8 * k + 7]) * scale);
+            reinterpret_cast<uint4 *>(dst)[k] = o;
+        }
+    } else if (part != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            reinterpret_cast<uint4 *>(part)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    }
+}
+
 // ------------------------------------------------------------------ launches
 struct FwdMaps {
     CUtensorMap q, k, k16, v, v16;  // boxes of a tile, and of 16 rows for narrow key blocks
@@ -279,7 +301,7 @@ struct FwdParams {
 
 struct BwdMaps {
     CUtensorMap x, y;       // stationary rows (128-row boxes): K, V or Q, dO
-    CUtensorMap u, w;       // streaming rows (64-row boxes): Q, dO or K, V
+    CUtensorMap u, w;       // streaming rows (boxes of a block): Q, dO or K, V
 };
 struct BwdParams {
     Common c;
@@ -311,13 +333,13 @@ struct SumParams {
 };
 
 int fwd_block(int d);  // keys of a key block
-int fwd_smem(int d);
-int bwd_smem(int d);
 cudaError_t fwd_prepare(int d, bool bf16);
-cudaError_t bwd_prepare(int d, bool bf16);
+cudaError_t dkv_prepare(int d, bool bf16);
+cudaError_t dq_prepare(int d, bool bf16);
 cudaError_t fwd_launch(int d, bool bf16, int grid, const FwdParams &p, const FwdMaps &m, cudaStream_t st);
 cudaError_t bwd_prep_launch(bool bf16, int n_tiles, const PrepParams &p, cudaStream_t st);
-cudaError_t bwd_launch(int d, bool bf16, bool keys, int grid, const BwdParams &p, const BwdMaps &m, cudaStream_t st);
+cudaError_t dkv_launch(int d, bool bf16, int grid, const BwdParams &p, const BwdMaps &m, cudaStream_t st);
+cudaError_t dq_launch(int d, bool bf16, int grid, const BwdParams &p, const BwdMaps &m, cudaStream_t st);
 cudaError_t bwd_sum_launch(bool bf16, int n_items, const SumParams &p, cudaStream_t st);
 
 }  // namespace window

@@ -1,32 +1,34 @@
-// window_bwd.cu -- gradient of the windowed attention (include/syn_window.h).
+// window_dkv.cu -- gradients of K and V of the windowed attention
+// (include/syn_window.h), the statistics they and window_dq.cu read, and the
+// joining of partial sums.
 //
 //   P = exp(scale S - lse),  dP = dO V^T,  dS = P * (dP - rowsum(dO * O))
-//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
+//   dV = P^T dO,  dK = scale dS^T Q
 //
-// One kernel in two forms, so that no sum needs atomics and the bits do not
-// depend on timing: the dK, dV form keeps 128 keys and streams query blocks
-// past them (all heads of the group, so shared heads sum in the accumulator),
-// the dQ form keeps 128 query rows and streams key blocks.  The scores are
-// computed in both (seven products where five are needed); writing the score
-// gradients out for the second product instead would move T * W elements a
-// head each way.  With X, Y the stationary tiles (K, V or Q, dO) and U, W the
-// streaming ones (Q, dO or K, V), a 64-row block does
+// No sum needs atomics, so the bits do not depend on timing: a CTA keeps 128
+// keys and streams query blocks of 64 rows past them, all heads of the group,
+// so that shared heads sum in the accumulator; dQ has a kernel of its own, which
+// computes the scores again (seven products where five are needed; writing the
+// score gradients out instead would move T * W elements a head each way).  With
+// X, Y the stationary tiles (K, V) and U, W the streaming ones (Q, dO), a block
+// does
 //
-//   S = X U^T, dP = Y W^T               128 x 64 each, into TMEM
-//   P, dS by the warpgroup g & 1        one stationary row per thread
-//   dV += P W (dK, dV form), dX += dS U  P and dS read from TMEM as 16-bit
+//   S = X U^T, dP = Y W^T   128 x 64 each, into TMEM
+//   P, dS                   by warpgroup g & 1: one key a thread
+//   dV += P W, dK += dS U   P and dS read from TMEM as 16-bit operands
 //
 //   warp 0        TMA producer: an item's X and Y, each block's U and W (ring)
 //   warps 1, 2    issue S = X U^T and dP = Y W^T
-//   warps 3, 4    issue dX += dS U and (dK, dV form) dY += P W
+//   warps 3, 4    issue dK += dS U and dV += P W
 //   warp 5        zeroes streaming rows past the sequence's end
 //   warps 8-11, 12-15  the two warpgroups
 //
 // TMEM (512 columns): three places of 64 for S, over which the block's P and dS
 // (32 each) stay until their sums are made; one place for dP, free again as
-// soon as the warpgroup has loaded it; sums at 256 and 384.  So three blocks are
-// under way at a time.  The dQ form has one sum and alternates between the two
-// places, so an item's output is read while the next item's products run.
+// soon as the warpgroup has loaded it; the sums at 256 and 384.  So three blocks
+// are under way at a time.  (Blocks of 128 queries, S and dP with P and dS over
+// them, had less to overlap: 1115 us against 928 at 16384 tokens, 32/8 heads of
+// 128, window 2048.)
 #include "window.cuh"
 
 namespace syn {
@@ -51,8 +53,8 @@ enum {
     B_PF = B_TL + 1,           // P, dS of block g written (3, g % 3)
     B_DN = B_PF + 3,           // sums updated by block g (3, g % 3; a commit of each sum's issuer)
     B_AF = B_DN + 3,           // an item's sums complete (a commit of each sum's issuer)
-    B_OE = B_AF + 1,           // sum place read out (2)
-    B_DRAIN = B_OE + 2,        // every MMA of an issuer completed (4)
+    B_OE = B_AF + 1,           // the item's sums read out
+    B_DRAIN = B_OE + 1,        // every MMA of an issuer completed (4)
     N_BAR = B_DRAIN + 4
 };
 
@@ -61,7 +63,7 @@ template <int D> struct Lay {
     static constexpr int kStage = 2 * kTileU;
     static constexpr int X = 0, Y = kTileX;
     static constexpr int RING = 2 * kTileX;
-    static constexpr int STAT = RING + kStages * kStage;  // [stage][2][64] -lse2, -delta (dK, dV form)
+    static constexpr int STAT = RING + kStages * kStage;  // [stage][2][64] -lse2, -delta
     static constexpr int BAR = STAT + kStages * 512;
     static constexpr int MISC = BAR + 8 * N_BAR;
     static constexpr int BYTES = MISC + 16 + 1024;
@@ -73,7 +75,7 @@ struct Blk {
     bool first, last;
 };
 
-template <bool KEYS> struct Walk {
+struct Walk {
     int i, end, b, h, n;
     const BwdItem *it;
     __device__ __forceinline__ void load(const BwdParams &p) {
@@ -81,9 +83,7 @@ template <bool KEYS> struct Walk {
         it = p.items + i;
         b = 0;
         h = it->h0;
-        // (query rows that see no key have one block without a valid row)
-        n = KEYS ? it->b1 - it->b0
-                 : max(1, (it->s_end + kBU - 1) / kBU + (it->k_end - it->w_lo + kBU - 1) / kBU);
+        n = it->b1 - it->b0;
     }
     __device__ __forceinline__ void init(const BwdParams &p) {
         i = p.begin[blockIdx.x];
@@ -92,30 +92,20 @@ template <bool KEYS> struct Walk {
         load(p);
     }
     __device__ __forceinline__ bool next(const BwdParams &p, Blk &k) {
-        if (i < end && (KEYS ? h == it->h1 : b == n)) {
+        if (i < end && h == it->h1) {
             ++i;
             load(p);
         }
         if (i >= end) return false;
         k.h = h;
-        if (KEYS) {
-            k.first = b == 0 && h == it->h0;
-            k.start = (it->b0 + b) * kBU;
-            k.valid = min(kBU, it->stream_len - k.start);
-            if (++b == n) {
-                b = 0;
-                ++h;
-            }
-            k.last = h == it->h1;
-        } else {
-            const int n_sink = (it->s_end + kBU - 1) / kBU;
-            const bool sink = b < n_sink;
-            k.first = b == 0;
-            k.start = sink ? b * kBU : it->w_lo + (b - n_sink) * kBU;
-            k.valid = min(kBU, (sink ? it->s_end : it->k_end) - k.start);
-            ++b;
-            k.last = b == n;
+        k.first = b == 0 && h == it->h0;
+        k.start = (it->b0 + b) * kBU;
+        k.valid = min(kBU, it->stream_len - k.start);
+        if (++b == n) {
+            b = 0;
+            ++h;
         }
+        k.last = h == it->h1;
         return true;
     }
 };
@@ -125,41 +115,8 @@ template <bool KEYS> struct Walk {
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 184;"); }
 
-// Probabilities and score gradients of columns 2K, 2K + 1 ..: 0 where not seen
-template <int K> struct PairRow {
-    static __device__ __forceinline__ void apply(uint32_t (&p)[32], uint32_t (&d)[32], const uint32_t (&seen)[2]) {
-        const uint32_t both = keep_if<2 * K % 32>(seen[K / 16], 0x0000ffffu, 0u) | keep_if<2 * K % 32 + 1>(seen[K / 16], 0xffff0000u, 0u);
-        p[K] &= both;
-        d[K] &= both;
-        if constexpr (K < 31) PairRow<K + 1>::apply(p, d, seen);
-    }
-};
-
-// 32 accumulator columns of this thread's row to 16-bit (dst) or fp32 (part)
-template <bool BF16>
-__device__ __forceinline__ void store_cols(uint32_t taddr, uint16_t *dst, float *part, float scale) {
-    uint32_t v[32];
-    ptx::tmem_ld_32x32b_x32(taddr, v);
-    ptx::tmem_ld_wait();
-    if (dst != nullptr) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint4 o;
-            o.x = pack16<BF16>(__uint_as_float(v[8 * k + 0]) * scale, __uint_as_float(v[8 * k + 1]) * scale);
-            o.y = pack16<BF16>(__uint_as_float(v[8 * k + 2]) * scale, __uint_as_float(v[8 * k + 3]) * scale);
-            o.z = pack16<BF16>(__uint_as_float(v[8 * k + 4]) * scale, __uint_as_float(v[8 * k + 5]) * scale);
-            o.w = pack16<BF16>(__uint_as_float(v[8 * k + 6]) * scale, __uint_as_float(v[8 * k + 7]) * scale);
-            reinterpret_cast<uint4 *>(dst)[k] = o;
-        }
-    } else if (part != nullptr) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            reinterpret_cast<uint4 *>(part)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-    }
-}
-
-template <int D, bool BF16, bool KEYS>
-__global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_constant__ BwdParams p,
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_constant__ BwdParams p,
                                                                  const __grid_constant__ BwdMaps m) {
     using L = Lay<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -175,10 +132,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
     if (threadIdx.x == 0) {
         *abort = 0;
         for (int i = 0; i < N_BAR; ++i) {
-            const bool four = i == B_TL || (i >= B_PF && i < B_PF + 3), eight = i >= B_OE && i < B_OE + 2;
+            const bool four = i == B_TL || (i >= B_PF && i < B_PF + 3), eight = i == B_OE;
             const bool products = i == B_XE || i == B_ZR || (i >= B_SF && i < B_SF + 6);
             const bool sums = (i >= B_DN && i < B_DN + 3) || i == B_AF || (i >= B_UE && i < B_UE + kStages);
-            ptx::mbar_init(bar(i), four ? 4 : eight ? 8 : products || (sums && KEYS) ? 2 : 1);
+            ptx::mbar_init(bar(i), four ? 4 : eight ? 8 : products || sums ? 2 : 1);
         }
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
@@ -195,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
     const uint32_t one = lane == 0 ? 1u : 0u;
     if (warp < 8) {
         regs_dec();
-        Walk<KEYS> wk;
+        Walk wk;
         wk.init(p);
         Blk b = {};
         if (warp == 0) {
@@ -205,11 +162,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
                 if (b.first) {
                     wait_bar(bar(B_XE), (ic & 1u) ^ 1u, abort, c);
                     if (lane == 0) {
-                        const int hx = KEYS ? wk.it->hk : b.h;
                         ptx::mbar_arrive_expect_tx(bar(B_XF), 2 * L::kTileX);
                         for (int x = 0; x < D / 64; ++x) {
-                            ptx::tma_load_3d(sbase + L::X + (uint32_t)(x * kBoxX), &m.x, bar(B_XF), x * 64, hx, wk.it->row0);
-                            ptx::tma_load_3d(sbase + L::Y + (uint32_t)(x * kBoxX), &m.y, bar(B_XF), x * 64, hx, wk.it->row0);
+                            ptx::tma_load_3d(sbase + L::X + (uint32_t)(x * kBoxX), &m.x, bar(B_XF), x * 64, wk.it->hk, wk.it->row0);
+                            ptx::tma_load_3d(sbase + L::Y + (uint32_t)(x * kBoxX), &m.y, bar(B_XF), x * 64, wk.it->hk, wk.it->row0);
                         }
                     }
                     ++ic;
@@ -218,17 +174,16 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
                 wait_bar(bar(B_UE + s), ((g / kStages) & 1u) ^ 1u, abort, c);
                 if (lane == 0) {
                     const uint32_t u = sbase + (uint32_t)(L::RING + s * L::kStage);
-                    const int hu = KEYS ? b.h : wk.it->hk, row = wk.it->stream0 + b.start;
-                    ptx::mbar_arrive_expect_tx(bar(B_UF + s), L::kStage + (KEYS ? 512 : 0));
+                    const int row = wk.it->stream0 + b.start;
+                    ptx::mbar_arrive_expect_tx(bar(B_UF + s), L::kStage + 512);
                     for (int x = 0; x < D / 64; ++x) {
-                        ptx::tma_load_3d(u + (uint32_t)(x * kBoxU), &m.u, bar(B_UF + s), x * 64, hu, row);
-                        ptx::tma_load_3d(u + (uint32_t)(L::kTileU + x * kBoxU), &m.w, bar(B_UF + s), x * 64, hu, row);
+                        ptx::tma_load_3d(u + (uint32_t)(x * kBoxU), &m.u, bar(B_UF + s), x * 64, b.h, row);
+                        ptx::tma_load_3d(u + (uint32_t)(L::kTileU + x * kBoxU), &m.w, bar(B_UF + s), x * 64, b.h, row);
                     }
-                    if (KEYS) {  // the block's statistics: 64 rows, aligned in the padded layout
-                        const int64_t o = (int64_t)b.h * p.pad_rows + wk.it->pad_row0 + b.start;
-                        ptx::bulk_g2s(sbase + (uint32_t)(L::STAT + s * 512), p.nlse2 + o, 256, bar(B_UF + s));
-                        ptx::bulk_g2s(sbase + (uint32_t)(L::STAT + s * 512 + 256), p.ndelta + o, 256, bar(B_UF + s));
-                    }
+                    // the block's statistics: 64 rows, aligned in the padded layout
+                    const int64_t o = (int64_t)b.h * p.pad_rows + wk.it->pad_row0 + b.start;
+                    ptx::bulk_g2s(sbase + (uint32_t)(L::STAT + s * 512), p.nlse2 + o, 256, bar(B_UF + s));
+                    ptx::bulk_g2s(sbase + (uint32_t)(L::STAT + s * 512 + 256), p.ndelta + o, 256, bar(B_UF + s));
                 }
                 __syncwarp();
             }
@@ -284,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
             // every MMA issued must complete before TMEM is released
             commit_if(one, bar(B_DRAIN + warp - 1));
             drain_bar(bar(B_DRAIN + warp - 1), 0, c);
-        } else if (warp == 3 || (KEYS && warp == 4)) {
+        } else if (warp <= 4) {
             // ================= dX += dS U (warp 3), dY += P W (warp 4) =================
             const bool is_y = warp == 4;
             constexpr uint32_t id_a = ptx::idesc_16bit_f32(BF16, 128, D, true);
@@ -292,13 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
             uint32_t g = 0, item = 0;
             for (; wk.next(p, b); ++g) {
                 const int s = (int)(g % kStages);
-                if (b.first) {  // the place's previous output has been read
-                    if (KEYS && item > 0) wait_bar(bar(B_OE), (item - 1u) & 1u, abort, c);
-                    if (!KEYS && item > 1) wait_bar(bar(B_OE + (int)(item & 1u)), ((item >> 1) - 1u) & 1u, abort, c);
-                }
+                if (b.first && item > 0) wait_bar(bar(B_OE), (item - 1u) & 1u, abort, c);  // the sums have been read out
                 const uint32_t u = u_d + (uint32_t)(s * L::kStage >> 4);
                 const uint32_t src = tmem + (g % 3u) * 64u + (is_y ? 0u : 32u);  // P, dS
-                const uint32_t dst = tmem + 256u + (is_y ? 128u : KEYS ? 0u : (item & 1u) * 128u);
+                const uint32_t dst = tmem + (is_y ? 384u : 256u);
                 wait_bar(bar(B_UF + s), (g / kStages) & 1u, abort, c);
                 wait_bar(bar(B_PF + (int)(g % 3u)), (g / 3u) & 1u, abort, c);
                 ptx::tc_fence_after();
@@ -323,24 +275,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
         const int row = qd * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)(qd * 32) << 16);
         const uint64_t scale2 = f2(c.scale_log2, c.scale_log2);
-        Walk<KEYS> wk;
+        Walk wk;
         wk.init(p);
         Blk b = {};
         uint32_t item = 0;
-        float nl = 0.f, nd = 0.f;  // dQ form: the row's -lse2, -delta
         for (uint32_t g = 0; wk.next(p, b); ++g) {
             const BwdItem &it = *wk.it;
-            if (!KEYS && b.first) {
-                const bool mine = row < it.n_rows;
-                const int64_t o = (int64_t)b.h * p.pad_rows + it.pad_row0 + (mine ? row : 0);
-                nl = mine ? p.nlse2[o] : -INFINITY;
-                nd = mine ? p.ndelta[o] : 0.f;
-            }
             if ((g & 1u) == (uint32_t)wg) {
                 const int s = (int)(g % kStages);
                 wait_bar(bar(B_SF + (int)(g % 6u)), (g / 6u) & 1u, abort, c);
                 const uint32_t ts = tl + (g % 3u) * 64u;
-                if (KEYS) wait_bar(bar(B_UF + s), (g / kStages) & 1u, abort, c);  // the statistics
+                wait_bar(bar(B_UF + s), (g / kStages) & 1u, abort, c);  // the statistics
                 ptx::tc_fence_after();
                 uint32_t sv[64], dv[64];
 #pragma unroll
@@ -353,53 +298,31 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
                 ptx::tc_fence_before();
                 __syncwarp();
                 arrive_if(one, bar(B_TL));
-                // columns [lo, hi) and those below sk are seen
-                const int pos = it.pos0 + row;
-                int lo, hi, sk = 0;
-                bool masked;
-                if (KEYS) {  // a key's row over query positions
-                    const int p0 = it.off + b.start;
-                    lo = clampi(pos - p0, 0, kBU);
-                    hi = pos < c.sinks ? kBU : clampi(pos + c.window - p0, 0, kBU);
-                    masked = p0 < it.pos0 + kBX - 1 || (it.pos0 <= p0 + kBU - 1 - c.window && it.pos0 + kBX > c.sinks);
-                } else {     // a query's row over keys
-                    hi = clampi(min(b.start + b.valid, pos + 1) - b.start, 0, kBU);
-                    lo = clampi(pos - c.window + 1 - b.start, 0, kBU);
-                    sk = clampi(c.sinks - b.start, 0, kBU);
-                    masked = b.valid < kBU || b.start + kBU - 1 > it.pos0 ||
-                             (b.start <= it.pos0 + kBX - 1 - c.window && b.start + kBU > c.sinks);
+                // this key is seen by the block's queries [lo, hi); scores of the others
+                // are -inf, so P and dS are 0 (rows past the end were zeroed: dP is 0 there)
+                const int pos = it.pos0 + row, p0 = it.off + b.start;
+                if (p0 < it.pos0 + kBX - 1 || (it.pos0 <= p0 + kBU - 1 - c.window && it.pos0 + kBX > c.sinks)) {
+                    const int lo = clampi(pos - p0, 0, kBU), hi = pos < c.sinks ? kBU : clampi(pos + c.window - p0, 0, kBU);
+                    const uint32_t seen[2] = {bits_below(hi, 0) & ~bits_below(lo, 0), bits_below(hi, 32) & ~bits_below(lo, 32)};
+                    MaskRow<0, kBU>::apply(sv, seen, __float_as_uint(-INFINITY));
                 }
                 const float4 *st_l = reinterpret_cast<const float4 *>(sm + L::STAT + s * 512);
                 uint32_t pk[32], dk[32];
 #pragma unroll
                 for (int k = 0; k < kBU; k += 4) {
-                    float4 a, d;
-                    if (KEYS) {
-                        a = st_l[k / 4];
-                        d = st_l[16 + k / 4];
-                    } else {
-                        a = make_float4(nl, nl, nl, nl);
-                        d = make_float4(nd, nd, nd, nd);
-                    }
+                    const float4 a = st_l[k / 4], d = st_l[16 + k / 4];
                     float x0, x1, x2, x3, y0, y1, y2, y3;
                     unf2(fma2(f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), scale2, f2(a.x, a.y)), x0, x1);
                     unf2(fma2(f2(__uint_as_float(sv[k + 2]), __uint_as_float(sv[k + 3])), scale2, f2(a.z, a.w)), x2, x3);
-                    float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
-                    unf2(mul2(f2(p0, p1), add2(f2(__uint_as_float(dv[k]), __uint_as_float(dv[k + 1])), f2(d.x, d.y))), y0, y1);
-                    unf2(mul2(f2(p2, p3), add2(f2(__uint_as_float(dv[k + 2]), __uint_as_float(dv[k + 3])), f2(d.z, d.w))), y2, y3);
-                    pk[k / 2] = pack16<BF16>(p0, p1);
-                    pk[k / 2 + 1] = pack16<BF16>(p2, p3);
+                    const float p0_ = ex2(x0), p1_ = ex2(x1), p2_ = ex2(x2), p3_ = ex2(x3);
+                    unf2(mul2(f2(p0_, p1_), add2(f2(__uint_as_float(dv[k]), __uint_as_float(dv[k + 1])), f2(d.x, d.y))), y0, y1);
+                    unf2(mul2(f2(p2_, p3_), add2(f2(__uint_as_float(dv[k + 2]), __uint_as_float(dv[k + 3])), f2(d.z, d.w))), y2, y3);
+                    pk[k / 2] = pack16<BF16>(p0_, p1_);
+                    pk[k / 2 + 1] = pack16<BF16>(p2_, p3_);
                     dk[k / 2] = pack16<BF16>(y0, y1);
                     dk[k / 2 + 1] = pack16<BF16>(y2, y3);
                 }
-                if (masked) {  // (pairs of 16 bits: a word's mask has both halves)
-                    uint32_t seen[2];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        seen[x] = bits_below(hi, 32 * x) & (~bits_below(lo, 32 * x) | bits_below(sk, 32 * x));
-                    PairRow<0>::apply(pk, dk, seen);
-                }
-                if (KEYS) ptx::tmem_st_32x32b_x32(ts, pk);
+                ptx::tmem_st_32x32b_x32(ts, pk);
                 ptx::tmem_st_32x32b_x32(ts + 32u, dk);
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
@@ -411,26 +334,19 @@ __global__ void __launch_bounds__(kThreads, 1) window_bwd_kernel(const __grid_co
                 ptx::tc_fence_after();
                 const bool mine = row < it.n_rows;
                 const int64_t r = it.row0 + row;
-                if (KEYS) {  // warpgroup 0 writes dK, warpgroup 1 dV
-                    const Out &o = wg == 0 ? p.dx : p.dy;
-                    uint16_t *dst = nullptr;
-                    float *part = nullptr;
-                    if (it.part >= 0) part = p.part + (((int64_t)it.part * 2 + wg) * kBX + row) * D;
-                    else if (mine) dst = static_cast<uint16_t *>(o.p) + r * o.token + it.hk * o.head;
+                // warpgroup 0 writes dK, warpgroup 1 dV
+                const Out &o = wg == 0 ? p.dx : p.dy;
+                uint16_t *dst = nullptr;
+                float *part = nullptr;
+                if (it.part >= 0) part = p.part + (((int64_t)it.part * 2 + wg) * kBX + row) * D;
+                else if (mine) dst = static_cast<uint16_t *>(o.p) + r * o.token + it.hk * o.head;
 #pragma unroll
-                    for (int x = 0; x < D / 32; ++x)
-                        store_cols<BF16>(tl + 256u + (uint32_t)(wg * 128 + x * 32), dst ? dst + x * 32 : nullptr,
-                                         part ? part + x * 32 : nullptr, wg == 0 ? c.scale : 1.f);
-                } else {     // each warpgroup half of dQ's columns
-                    uint16_t *dst = mine ? static_cast<uint16_t *>(p.dx.p) + r * p.dx.token + b.h * p.dx.head + wg * (D / 2) : nullptr;
-#pragma unroll
-                    for (int x = 0; x < D / 64; ++x)
-                        store_cols<BF16>(tl + 256u + (item & 1u) * 128u + (uint32_t)(wg * (D / 2) + x * 32),
-                                         dst ? dst + x * 32 : nullptr, nullptr, c.scale);
-                }
+                for (int x = 0; x < D / 32; ++x)
+                    store_cols<BF16>(tl + 256u + (uint32_t)(wg * 128 + x * 32), dst ? dst + x * 32 : nullptr,
+                                     part ? part + x * 32 : nullptr, wg == 0 ? c.scale : 1.f);
                 ptx::tc_fence_before();
                 __syncwarp();
-                arrive_if(one, bar(B_OE + (KEYS ? 0 : (int)(item & 1u))));
+                arrive_if(one, bar(B_OE));
                 ++item;
             }
         }
@@ -512,35 +428,24 @@ template <bool BF16> __global__ void __launch_bounds__(256) window_sum_kernel(co
     }
 }
 
-template <int D, bool BF16, bool KEYS>
-cudaError_t launch(int grid, const BwdParams &p, const BwdMaps &m, cudaStream_t st) {
-    window_bwd_kernel<D, BF16, KEYS><<<grid, kThreads, Lay<D>::BYTES, st>>>(p, m);
+template <int D, bool BF16> cudaError_t launch(int grid, const BwdParams &p, const BwdMaps &m, cudaStream_t st) {
+    window_dkv_kernel<D, BF16><<<grid, kThreads, Lay<D>::BYTES, st>>>(p, m);
     return cudaGetLastError();
 }
 template <int D, bool BF16> cudaError_t prepare() {
-    cudaError_t e = cudaFuncSetAttribute(window_bwd_kernel<D, BF16, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Lay<D>::BYTES);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(window_bwd_kernel<D, BF16, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Lay<D>::BYTES);
+    return cudaFuncSetAttribute(window_dkv_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::BYTES);
 }
 
 }  // namespace
 
-int bwd_smem(int d) { return d == 64 ? Lay<64>::BYTES : Lay<128>::BYTES; }
-
-cudaError_t bwd_prepare(int d, bool bf16) {
+cudaError_t dkv_prepare(int d, bool bf16) {
     if (d == 64) return bf16 ? prepare<64, true>() : prepare<64, false>();
     return bf16 ? prepare<128, true>() : prepare<128, false>();
 }
 
-cudaError_t bwd_launch(int d, bool bf16, bool keys, int grid, const BwdParams &p, const BwdMaps &m, cudaStream_t st) {
-    if (d == 64) {
-        if (bf16) return keys ? launch<64, true, true>(grid, p, m, st) : launch<64, true, false>(grid, p, m, st);
-        return keys ? launch<64, false, true>(grid, p, m, st) : launch<64, false, false>(grid, p, m, st);
-    }
-    if (bf16) return keys ? launch<128, true, true>(grid, p, m, st) : launch<128, true, false>(grid, p, m, st);
-    return keys ? launch<128, false, true>(grid, p, m, st) : launch<128, false, false>(grid, p, m, st);
+cudaError_t dkv_launch(int d, bool bf16, int grid, const BwdParams &p, const BwdMaps &m, cudaStream_t st) {
+    if (d == 64) return bf16 ? launch<64, true>(grid, p, m, st) : launch<64, false>(grid, p, m, st);
+    return bf16 ? launch<128, true>(grid, p, m, st) : launch<128, false>(grid, p, m, st);
 }
 
 cudaError_t bwd_prep_launch(bool bf16, int n_tiles, const PrepParams &p, cudaStream_t st) {

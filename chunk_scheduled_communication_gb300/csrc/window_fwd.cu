@@ -132,9 +132,9 @@ template <bool BF16, int D> __device__ __forceinline__ void store_row(void *dst_
 }
 
 // Register split: the launch gives 128 a thread (512 threads); the first eight
-// warps keep 72, the softmax warps take 184: 256 * 72 + 256 * 184 = 65,536.
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 184;"); }
+// warps keep 64, the softmax warps take 192: 256 * 64 + 256 * 192 = 65,536.
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 192;"); }
 
 template <int V> struct Int {
     static constexpr int value = V;
@@ -468,8 +468,6 @@ template <int D, bool BF16> cudaError_t prepare() {
 }  // namespace
 
 int fwd_block(int d) { return d == 64 ? Lay<64>::kBK : Lay<128>::kBK; }
-int fwd_smem(int d) { return d == 64 ? Lay<64>::BYTES : Lay<128>::BYTES; }
-
 cudaError_t fwd_prepare(int d, bool bf16) {
     if (d == 64) return bf16 ? prepare<64, true>() : prepare<64, false>();
     return bf16 ? prepare<128, true>() : prepare<128, false>();
