@@ -289,15 +289,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
                 ptx::tc_fence_after();
                 uint32_t sv[64], dv[64];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    ptx::tmem_ld_32x32b_x32(ts + (uint32_t)(x * 32), *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * x));
+                for (int x = 0; x < 2; ++x)
                     ptx::tmem_ld_32x32b_x32(tl + 192u + (uint32_t)(x * 32), *reinterpret_cast<uint32_t(*)[32]>(dv + 32 * x));
-                }
                 ptx::tmem_ld_wait();
-                // (the next block's dP may take its place)
+                // dP first: the next block's may take its place
                 ptx::tc_fence_before();
                 __syncwarp();
                 arrive_if(one, bar(B_TL));
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    ptx::tmem_ld_32x32b_x32(ts + (uint32_t)(x * 32), *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * x));
+                ptx::tmem_ld_wait();
                 // this key is seen by the block's queries [lo, hi); scores of the others
                 // are -inf, so P and dS are 0 (rows past the end were zeroed: dP is 0 there)
                 const int pos = it.pos0 + row, p0 = it.off + b.start;
@@ -360,44 +362,61 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
 }
 
 // -lse log2(e) and -rowsum(dO * O) of each row and head into [head][padded row],
-// so that a block's 64 statistics are one aligned run.  Eight lanes a row.
-template <bool BF16> __global__ void __launch_bounds__(256) window_prep_kernel(const __grid_constant__ PrepParams p) {
+// so that a block's 64 statistics are one aligned run.  Eight lanes a row; a
+// group's kPrepRows rows are loaded together (HBM bounds the long inputs, the
+// latency of a load the short ones).
+constexpr int kPrepRows = 4;
+template <bool BF16, int D> __global__ void __launch_bounds__(256) window_prep_kernel(const __grid_constant__ PrepParams p) {
     const PrepTile t = p.tiles[blockIdx.x];
     const int sub = (int)threadIdx.x & 7, grp = (int)threadIdx.x >> 3;
     const uint32_t mask = 0xffu << (threadIdx.x & 24u);
-    for (int i = (int)blockIdx.y * 32 + grp; i < 64 * p.H_q; i += (int)gridDim.y * 32) {
-        const int r = i / p.H_q, h = i - r * p.H_q;
-        float v = 0.f, nl = -INFINITY;
-        if (r < t.n_rows) {
-            const int64_t row = t.row0 + r;
-            const uint16_t *a = static_cast<const uint16_t *>(p.o) + row * p.o_token + h * p.o_head;
-            const uint16_t *b = static_cast<const uint16_t *>(p.d_o) + row * p.do_token + h * p.do_head;
-            const float l = p.lse[row * p.H_q + h];
-            if (l != -INFINITY) {
-                nl = -l * 1.4426950408889634f;
-                for (int k = sub * 8; k < p.d; k += 64) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(a + k), y = *reinterpret_cast<const uint4 *>(b + k);
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    uint4 x[kPrepRows][D / 64], y[kPrepRows][D / 64];
+    float l[kPrepRows];
+    int r[kPrepRows], h[kPrepRows];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float2 u, w;
-                        if (BF16) {
-                            u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&xs[j]));
-                            w = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&ys[j]));
-                        } else {
-                            u = __half22float2(*reinterpret_cast<const __half2 *>(&xs[j]));
-                            w = __half22float2(*reinterpret_cast<const __half2 *>(&ys[j]));
-                        }
-                        v = fmaf(u.x, w.x, fmaf(u.y, w.y, v));
+    for (int u = 0; u < kPrepRows; ++u) {
+        const int i = ((int)blockIdx.y * kPrepRows + u) * 32 + grp;
+        r[u] = i / p.H_q;
+        h[u] = i - r[u] * p.H_q;
+        l[u] = -INFINITY;
+        if (r[u] < t.n_rows) {
+            const int64_t row = t.row0 + r[u];
+            const uint16_t *a = static_cast<const uint16_t *>(p.o) + row * p.o_token + h[u] * p.o_head + sub * 8;
+            const uint16_t *b = static_cast<const uint16_t *>(p.d_o) + row * p.do_token + h[u] * p.do_head + sub * 8;
+            l[u] = p.lse[row * p.H_q + h[u]];
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) {
+                x[u][k] = *reinterpret_cast<const uint4 *>(a + k * 64);
+                y[u][k] = *reinterpret_cast<const uint4 *>(b + k * 64);
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kPrepRows; ++u) {
+        float v = 0.f;
+        if (l[u] != -INFINITY) {  // (a row that sees no key has no gradient)
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) {
+                const uint32_t xs[4] = {x[u][k].x, x[u][k].y, x[u][k].z, x[u][k].w}, ys[4] = {y[u][k].x, y[u][k].y, y[u][k].z, y[u][k].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float2 e, f;
+                    if (BF16) {
+                        e = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&xs[j]));
+                        f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&ys[j]));
+                    } else {
+                        e = __half22float2(*reinterpret_cast<const __half2 *>(&xs[j]));
+                        f = __half22float2(*reinterpret_cast<const __half2 *>(&ys[j]));
                     }
+                    v = fmaf(e.x, f.x, fmaf(e.y, f.y, v));
                 }
             }
         }
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(mask, v, o);
-        if (sub == 0) {
-            const int64_t at = (int64_t)h * p.pad_rows + t.pad_row0 + r;
-            p.nlse2[at] = nl;
+        if (sub == 0 && r[u] < 64) {
+            const int64_t at = (int64_t)h[u] * p.pad_rows + t.pad_row0 + r[u];
+            p.nlse2[at] = l[u] == -INFINITY ? -INFINITY : -1.4426950408889634f * l[u];
             p.ndelta[at] = -v;
         }
     }
@@ -406,10 +425,11 @@ template <bool BF16> __global__ void __launch_bounds__(256) window_prep_kernel(c
 // dK, dV tiles that were summed in parts: the parts in their fixed order
 template <bool BF16> __global__ void __launch_bounds__(256) window_sum_kernel(const __grid_constant__ SumParams p) {
     const SumItem it = p.items[blockIdx.x];
-    const int per = p.d / 8;
-    for (int i = (int)threadIdx.x; i < it.n_rows * per; i += 256) {
-        const int r = i / per, k = (i - r * per) * 8;
+    const int per = p.d / 8, rows = 256 / per;  // rows of a block: one vector of eight a thread
+    const int r = (int)blockIdx.z * rows + (int)threadIdx.x / per, k = (int)threadIdx.x % per * 8;
+    if (r < it.n_rows) {
         float v[8] = {};
+#pragma unroll 4
         for (int j = 0; j < it.n_parts; ++j) {
             const float4 *src = reinterpret_cast<const float4 *>(
                 p.part + (((int64_t)(it.part0 + j) * 2 + blockIdx.y) * kBX + r) * p.d + k);
@@ -449,15 +469,19 @@ cudaError_t dkv_launch(int d, bool bf16, int grid, const BwdParams &p, const Bwd
 }
 
 cudaError_t bwd_prep_launch(bool bf16, int n_tiles, const PrepParams &p, cudaStream_t st) {
-    // a block takes up to 8 rows of heads per group of lanes
-    const dim3 grid((unsigned)n_tiles, (unsigned)((64 * p.H_q + 255) / 256));
-    if (bf16) window_prep_kernel<true><<<grid, 256, 0, st>>>(p);
-    else window_prep_kernel<false><<<grid, 256, 0, st>>>(p);
+    const dim3 grid((unsigned)n_tiles, (unsigned)((64 * p.H_q + 32 * kPrepRows - 1) / (32 * kPrepRows)));
+    if (p.d == 64) {
+        if (bf16) window_prep_kernel<true, 64><<<grid, 256, 0, st>>>(p);
+        else window_prep_kernel<false, 64><<<grid, 256, 0, st>>>(p);
+    } else {
+        if (bf16) window_prep_kernel<true, 128><<<grid, 256, 0, st>>>(p);
+        else window_prep_kernel<false, 128><<<grid, 256, 0, st>>>(p);
+    }
     return cudaGetLastError();
 }
 
 cudaError_t bwd_sum_launch(bool bf16, int n_items, const SumParams &p, cudaStream_t st) {
-    const dim3 grid((unsigned)n_items, 2);
+    const dim3 grid((unsigned)n_items, 2, (unsigned)(kBX * p.d / 8 / 256));
     if (bf16) window_sum_kernel<true><<<grid, 256, 0, st>>>(p);
     else window_sum_kernel<false><<<grid, 256, 0, st>>>(p);
     return cudaGetLastError();
