@@ -36,8 +36,8 @@ constexpr int kRowsM = 16;         // query heads of a CTA
 constexpr int kDecStages = 2;
 constexpr int kDecCtas = 3;        // resident on an SM
 constexpr int kMaxSplits = 128;
-constexpr int kWaves = 4;          // CTAs wanted per resident slot
-constexpr int kMinTiles = 2;       // tiles of a range at least, where there are that many
+constexpr int kWaves = 6;          // CTAs wanted per resident slot
+constexpr int kMinTiles = 1;       // tiles of a range at least, where there are that many
 
 struct DecParams {
     const void *q, *k, *v;
