@@ -36,7 +36,8 @@ constexpr int kThreads = 256;
 constexpr int kMaxD = 256;
 constexpr int kRowsPerLane = 4;     // rows whose loads a lane has under way at long inputs
 constexpr int kGradRowsPerLane = 3; // (gradient: of the step ahead)
-constexpr int kGradBlocksPerSm = 2; // persistent blocks of the gradient kernel
+constexpr int kGradThreads = 128;
+constexpr int kGradBlocksPerSm = 4; // persistent blocks of the gradient kernel
 constexpr int kTableBytes = 14 * 1024;  // cosines and sines of a block's tokens at most
 
 struct Tensor {
@@ -188,21 +189,21 @@ __device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_g
 template <int N> __device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // A lane's slots of a row: staged as [slot][2][thread] packs, then widened
-template <typename T, int VEC, int L, int NS>
+template <int TH, typename T, int VEC, int L, int NS>
 __device__ __forceinline__ void stage_row(Pack<T, VEC> *st, const T *row, const Slots<VEC, L, NS> &s) {
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
-        if (s.has0[n]) stage(st + (2 * n) * kThreads + threadIdx.x, row + s.o0[n]);
-        if (s.has1[n]) stage(st + (2 * n + 1) * kThreads + threadIdx.x, row + s.o1[n]);
+        if (s.has0[n]) stage(st + (2 * n) * TH + threadIdx.x, row + s.o0[n]);
+        if (s.has1[n]) stage(st + (2 * n + 1) * TH + threadIdx.x, row + s.o1[n]);
     }
 }
 
-template <typename T, int VEC, int L, int NS>
+template <int TH, typename T, int VEC, int L, int NS>
 __device__ __forceinline__ void widen(float (&e)[NS][2 * VEC], const Pack<T, VEC> *st, const Slots<VEC, L, NS> &s) {
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
-        st[(2 * n) * kThreads + threadIdx.x].widen(e[n]);
-        st[(2 * n + 1) * kThreads + threadIdx.x].widen(e[n] + VEC);
+        st[(2 * n) * TH + threadIdx.x].widen(e[n]);
+        st[(2 * n + 1) * TH + threadIdx.x].widen(e[n] + VEC);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
             if (!s.has0[n]) e[n][i] = 0.f;
@@ -218,9 +219,10 @@ __device__ __forceinline__ uint32_t divide(uint32_t r, uint32_t magic, uint32_t 
 
 // The cosines and sines of tokens tok0 .. tok0 + n - 1, times the factor, by the
 // whole block: table[token][2][d_rot / 2].
+template <int TH>
 __device__ __forceinline__ void fill_table(float *table, const Args &a, uint32_t tok0, uint32_t n) {
     const uint32_t half = (uint32_t)a.d_rot / 2;
-    for (uint32_t i = threadIdx.x; i < n * half; i += kThreads) {
+    for (uint32_t i = threadIdx.x; i < n * half; i += TH) {
         const uint32_t t = i / half, f = i - t * half;
         const int64_t pos = a.pos != nullptr ? a.pos[tok0 + t] : a.pos0 + (int64_t)(tok0 + t);
         const uint64_t turn = (uint64_t)pos * a.step[f];
@@ -324,7 +326,7 @@ template <int NS, int E> __device__ __forceinline__ float squares(const float (&
 
 // Shared memory for the gradient's staged rows, or its sums where they are more
 template <typename T, int VEC, int NS, int U> __host__ __device__ constexpr int grad_stage_bytes() {
-    const int rows = 2 * U * 2 * 2 * NS * kThreads * (int)sizeof(Pack<T, VEC>), sums = kThreads * NS * 2 * VEC * 4;
+    const int rows = 2 * U * 2 * 2 * NS * kGradThreads * (int)sizeof(Pack<T, VEC>), sums = kGradThreads * NS * 2 * VEC * 4;
     return ((rows > sums ? rows : sums) + 15) / 16 * 16;
 }
 
@@ -351,19 +353,17 @@ __global__ void __launch_bounds__(kThreads, NORM ? 4 : 5) rope_kernel(const __gr
         const int64_t xt = t.xt, xh = t.xh, yt = t.yt, yh = t.yh;
         Slots<VEC, L, NS> s;
         s.init(a, copy, sub);
-        float w[NS][2 * VEC];
-        if (norm) load_weight<T>(w, t.w, s);
         for (uint32_t r0 = grp; r0 - grp < rows; r0 += G * U) {
             uint32_t tok[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const uint32_t r = r0 + u * G;
                 tok[u] = divide(r, magic, shift);
-                if (r < rows) stage_row(staged[u], src + (int64_t)tok[u] * xt + (int64_t)(r - tok[u] * heads) * xh, s);
+                if (r < rows) stage_row<kThreads>(staged[u], src + (int64_t)tok[u] * xt + (int64_t)(r - tok[u] * heads) * xh, s);
             }
             stage_commit();
             if (!filled) {
-                fill_table(table, a, tok0, n_tok);
+                fill_table<kThreads>(table, a, tok0, n_tok);
                 __syncthreads();
                 filled = true;
             }
@@ -378,9 +378,11 @@ __global__ void __launch_bounds__(kThreads, NORM ? 4 : 5) rope_kernel(const __gr
                     if (to < 0 || to >= a.n_slots) continue;
                 }
                 float e[NS][2 * VEC];
-                widen(e, staged[u], s);
+                widen<kThreads>(e, staged[u], s);
                 if (norm) {
                     const float inv = rsqrtf(group_sum<L>(squares(e), mask) * a.inv_d + a.eps);
+                    float w[NS][2 * VEC];  // (read for each row, from L1: kept, it costs a block an SM)
+                    load_weight<T>(w, t.w, s);
 #pragma unroll
                     for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -403,9 +405,9 @@ __global__ void __launch_bounds__(kThreads, NORM ? 4 : 5) rope_kernel(const __gr
 // blocks are persistent, so that there are few partial sums, and each step's
 // rows are staged while the step before is computed.
 template <typename T, int VEC, int L, int NS, int U>
-__global__ void __launch_bounds__(kThreads, kGradBlocksPerSm) norm_grad_kernel(const __grid_constant__ Args a) {
-    constexpr int G = kThreads / L;
-    constexpr int kSlots = 2 * NS * kThreads;
+__global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm) norm_grad_kernel(const __grid_constant__ Args a) {
+    constexpr int G = kGradThreads / L;
+    constexpr int kSlots = 2 * NS * kGradThreads;
     extern __shared__ __align__(16) uint8_t sm[];
     Pack<T, VEC> *staged = reinterpret_cast<Pack<T, VEC> *>(sm);               // [2][U][x, dy][slots]
     float *sums = reinterpret_cast<float *>(sm);                               // [group][element], at the end
@@ -437,8 +439,8 @@ __global__ void __launch_bounds__(kThreads, kGradBlocksPerSm) norm_grad_kernel(c
                     const uint32_t tok = divide(r, magic, shift);
                     const int64_t h = (int64_t)(r - tok * heads);
                     Pack<T, VEC> *st = staged + (half * U + u) * 2 * kSlots;
-                    stage_row(st, src + (int64_t)tok * xt + h * xh, s);
-                    stage_row(st + kSlots, grd + (int64_t)tok * gt + h * gh, s);
+                    stage_row<kGradThreads>(st, src + (int64_t)tok * xt + h * xh, s);
+                    stage_row<kGradThreads>(st + kSlots, grd + (int64_t)tok * gt + h * gh, s);
                 }
             }
             stage_commit();
@@ -450,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, kGradBlocksPerSm) norm_grad_kernel(c
             const uint32_t r1 = min(r0 + per, rows), tok0 = divide(r0, magic, shift);
             issue(r0 + step < rows ? r0 + step : rows, half ^ 1u);
             float *tab = table + half * a.table_tokens * (uint32_t)a.d_rot;
-            fill_table(tab, a, tok0, divide(r1 - 1, magic, shift) - tok0 + 1);
+            fill_table<kGradThreads>(tab, a, tok0, divide(r1 - 1, magic, shift) - tok0 + 1);
             __syncthreads();
             stage_wait<1>();
 #pragma unroll
@@ -462,11 +464,11 @@ __global__ void __launch_bounds__(kThreads, kGradBlocksPerSm) norm_grad_kernel(c
                 float e[NS][2 * VEC], g[NS][2 * VEC];
                 {
                     float cs[NS][VEC], sn[NS][VEC];
-                    widen(g, st + kSlots, s);
+                    widen<kGradThreads>(g, st + kSlots, s);
                     read_table(cs, sn, tab, a, tok - tok0, s);
                     turn(g, cs, sn, a, s);
                 }
-                widen(e, st, s);
+                widen<kGradThreads>(e, st, s);
                 float gw[NS][2 * VEC];
                 uint64_t m2 = f2(0.f, 0.f);  // sums of g w x
 #pragma unroll
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, kGradBlocksPerSm) norm_grad_kernel(c
                 if (s.has1[n]) sums[grp * a.d + s.o1[n] + i] = acc[n][VEC + i];
             }
         __syncthreads();
-        for (int j = (int)threadIdx.x; j < a.d; j += kThreads) {
+        for (int j = (int)threadIdx.x; j < a.d; j += kGradThreads) {
             float v = 0.f;
             for (int k = 0; k < G; ++k) v += sums[k * a.d + j];
             a.partial[((int64_t)blockIdx.x * 2 + x) * kMaxD + j] = v;
@@ -625,7 +627,7 @@ template <typename T, int VEC, int L, int NS, int U, bool NORM> int launch_forwa
 template <typename T, int VEC, int L, int NS> int launch(syn_rope_plan_s *pl, Args &a, Kind kind, cudaStream_t st, int &grid) {
     constexpr int G = kThreads / L, kMany = VEC == 1 ? 1 : kRowsPerLane;
     if (kind == kNormGrad) {
-        constexpr int U = VEC == 1 ? 1 : kGradRowsPerLane;
+        constexpr int U = VEC == 1 ? 1 : kGradRowsPerLane, G = kGradThreads / L;
         a.table_tokens = 1;
         int64_t blocks = 1;
         for (int x = 0; x < a.n_tensors; ++x) {
@@ -636,7 +638,7 @@ template <typename T, int VEC, int L, int NS> int launch(syn_rope_plan_s *pl, Ar
         grid = (int)std::min<int64_t>(blocks, (int64_t)pl->num_sms * kGradBlocksPerSm);
         const size_t smem = (size_t)grad_stage_bytes<T, VEC, NS, U>() + (size_t)a.table_tokens * (size_t)a.d_rot * 8;
         ROPE_CK(cudaFuncSetAttribute(norm_grad_kernel<T, VEC, L, NS, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-        norm_grad_kernel<T, VEC, L, NS, U><<<grid, kThreads, smem, st>>>(a);
+        norm_grad_kernel<T, VEC, L, NS, U><<<grid, kGradThreads, smem, st>>>(a);
         ROPE_CK(cudaGetLastError());
         return SYN_OK;
     }
