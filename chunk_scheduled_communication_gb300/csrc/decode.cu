@@ -334,15 +334,15 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) window_decode_kernel(co
     if (p.splits == 1) return;
     // the range that arrives last joins all of them, in their order
     __shared__ uint32_t last;
-    __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
+        __threadfence();  // (the block's partial results, seen through the barrier)
         last = ptx::atom_add_acq_rel_gpu(p.arrived + slot_id, 1u) == (uint32_t)p.splits - 1u;
         if (last) p.arrived[slot_id] = 0u;  // for the next call
+        __threadfence();
     }
     __syncthreads();
     if (!last) return;
-    __threadfence();
     // each range's factor exp2(m - top) and the sums, all loads at once
     float *fm = reinterpret_cast<float *>(sm), *fl = fm + kMaxSplits * kRowsM;  // [split][16]
     for (int i = (int)threadIdx.x; i < p.splits * kRowsM; i += kDecThreads) {

@@ -516,18 +516,18 @@ int syn_window_attention_backward(syn_window_plan_t pl, const syn_window_rows_t 
             (rc = encode(&queries.x, pl, *Q, nq, c.H_q, 128)) != SYN_OK || (rc = encode(&queries.y, pl, *dO, nq, c.H_q, 128)) != SYN_OK ||
             (rc = encode(&queries.u, pl, *K, nk, c.H_kv, 128)) != SYN_OK || (rc = encode(&queries.w, pl, *V, nk, c.H_kv, 128)) != SYN_OK)
             return rc;
+        if (pl->grid_q > 0) {
+            p.items = pl->d_query_items;
+            p.begin = pl->d_query_begin;
+            p.dx = out_of(dQ);
+            WIN_CK(dq_launch(c.d, pl->bf16, pl->grid_q, p, queries, st));
+        }
         if (pl->grid_k > 0) {
             p.items = pl->d_key_items;
             p.begin = pl->d_key_begin;
             p.dx = out_of(dK);
             p.dy = out_of(dV);
             WIN_CK(dkv_launch(c.d, pl->bf16, pl->grid_k, p, keys, st));
-        }
-        if (pl->grid_q > 0) {
-            p.items = pl->d_query_items;
-            p.begin = pl->d_query_begin;
-            p.dx = out_of(dQ);
-            WIN_CK(dq_launch(c.d, pl->bf16, pl->grid_q, p, queries, st));
         }
     } else if (nq > 0) {  // no key at all: dQ = 0
         for (int h = 0; h < c.H_q; ++h)

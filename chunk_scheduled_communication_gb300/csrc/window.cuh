@@ -307,7 +307,8 @@ struct BwdParams {
     Common c;
     const BwdItem *items;
     const int32_t *begin;   // [grid + 1]
-    const float *nlse2, *ndelta;  // [H_q][pad_rows]: -lse * log2(e) (-inf: no gradient), -rowsum(dO * O)
+    const float *nlse2;     // [H_q][pad_rows]: -lse * log2(e) (-inf: no gradient)
+    float *ndelta;          // [H_q][pad_rows]: -rowsum(dO * O); the dQ kernel makes some of them exact
     int64_t pad_rows;
     Out dx, dy;             // dK, dV or dQ
     float *part;            // [parts][2][128][d]

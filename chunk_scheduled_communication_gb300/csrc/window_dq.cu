@@ -18,6 +18,12 @@
 // TMEM (512 columns): S at 0, free again once loaded; dP at 128 or 256 in turn
 // with dS over it; the sum at 384.  W is free as soon as dP is made, U when dQ
 // is, so U has three stages and W two.
+//
+// rowsum(dO O) comes from the stored O, whose rounding is that of a whole value
+// row where a query sees few keys: there P dP - P rowsum nearly cancels and the
+// rounding shows.  A tile that sees one block only has its row's P and dP at
+// hand, so it takes rowsum(P dP) instead and leaves it for dK and dV, whose
+// kernel runs after this one.
 #include "window.cuh"
 
 namespace syn {
@@ -55,7 +61,8 @@ template <int D> struct Lay {
     static constexpr int X = 0, Y = kTile;
     static constexpr int U = 2 * kTile;
     static constexpr int W = U + kUStages * kTile;
-    static constexpr int BAR = W + kWStages * kTile;
+    static constexpr int SUM = W + kWStages * kTile;  // [2][128] halves of rowsum(P dP)
+    static constexpr int BAR = SUM + 2 * 128 * 4;
     static constexpr int MISC = BAR + 8 * N_BAR;
     static constexpr int BYTES = MISC + 16 + 1024;
 };
@@ -298,7 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_con
             const bool mine = row < it.n_rows;
             const int64_t o = (int64_t)it.h0 * p.pad_rows + it.pad_row0 + (mine ? row : 0);
             const float nl = mine ? p.nlse2[o] : -INFINITY, nd = mine ? p.ndelta[o] : 0.f;
-            const uint64_t nl2 = f2(nl, nl), nd2 = f2(nd, nd);
+            const uint64_t nl2 = f2(nl, nl);
+            uint64_t nd2 = f2(nd, nd);
             for (int k = 0; k < n; ++k, ++g) {
                 step(b, k, n_sink, it);
                 const uint32_t t_d = tl + (uint32_t)(128 + co) + (g & 1u) * 128u;
@@ -338,6 +346,23 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_con
                 for (int x = 0; x < 2; ++x)
                     ptx::tmem_ld_32x32b_x32(t_d + (uint32_t)(x * 32), *reinterpret_cast<uint32_t(*)[32]>(d + 32 * x));
                 ptx::tmem_ld_wait();
+                if (n == 1) {
+                    MaskRow<0, 64>::apply(d, seen, __float_as_uint(-nd));
+                    uint64_t sum = f2(0.f, 0.f);
+#pragma unroll
+                    for (int j = 0; j < 64; j += 2)
+                        sum = fma2(f2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
+                                   add2(f2(__uint_as_float(d[j]), __uint_as_float(d[j + 1])), nd2), sum);
+                    float s0, s1;
+                    unf2(sum, s0, s1);
+                    float *halves = reinterpret_cast<float *>(sm + L::SUM);
+                    halves[wg * 128 + row] = s0 + s1;
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                    const float exact = nd - (halves[row] + halves[128 + row]);  // (the halves in their order)
+                    asm volatile("bar.sync 1, 256;" ::: "memory");               // (read before they are replaced)
+                    nd2 = f2(exact, exact);
+                    if (wg == 0 && mine) p.ndelta[o] = exact;
+                }
                 uint32_t pk[32];
 #pragma unroll
                 for (int j = 0; j < 64; j += 2) {

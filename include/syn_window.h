@@ -23,8 +23,9 @@
  * in the gradient the score gradients) are rounded to the inputs' type as
  * operands of the next product; outputs are rounded once.  A value row V[j]
  * that is not finite reaches the rows of every 128-row query tile that reads
- * its block, as 0 * inf does in a matrix product; rows outside a sequence
- * (another sequence's, an unused part of a page) never do.
+ * its block, as 0 * inf does in a matrix product, and a query or dO row that is
+ * not finite the gradients of the keys in the tiles that its block meets; rows
+ * outside a sequence (another sequence's, an unused part of a page) never do.
  */
 #ifndef SYN_WINDOW_H
 #define SYN_WINDOW_H
