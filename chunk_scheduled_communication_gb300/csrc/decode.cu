@@ -13,6 +13,12 @@
 // the tensor pipe is far from the bound).  The warps join through shared
 // memory, the ranges through a workspace in the CTA that arrives last, in the
 // ranges' order.
+//
+// Measured on one GB300 (bf16, 32/8 heads of 128): 128 sequences at window 4096,
+// 2.15 GB of visible rows, 355 us, 6.05 TB/s, 0.89 of the measured copy rate
+// (two stages and three CTAs an SM; three and two 419 us, six and one 802 us);
+// three sequences at window 1024 12.5 to 13.5 us, a chain of dependent loads
+// (length, page, row), the join through memory and the launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

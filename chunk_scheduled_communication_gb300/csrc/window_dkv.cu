@@ -26,9 +26,14 @@
 // TMEM (512 columns): three places of 64 for S, over which the block's P and dS
 // (32 each) stay until their sums are made; one place for dP, free again as
 // soon as the warpgroup has loaded it; the sums at 256 and 384.  So three blocks
-// are under way at a time.  (Blocks of 128 queries, S and dP with P and dS over
-// them, had less to overlap: 1115 us against 928 at 16384 tokens, 32/8 heads of
-// 128, window 2048.)
+// are under way at a time.
+//
+// Measured on one GB300 (bf16, 16384 tokens, 32/8 heads of 128, window 2048, 4
+// sinks): 855 us, tensor pipe 55 % active.  It is bound by the round trip of dP's
+// one place -- product, commit, load, arrival -- beside products of 64 columns,
+// which cost the pipe 48 to 58 cycles where 32 would be the peak's pace.  Blocks
+// of 128 queries, S and dP with P and dS over them, had less to overlap (1115
+// us); S and dP issued by one warp, dP first, 1290 us.
 #include "window.cuh"
 
 namespace syn {

@@ -24,6 +24,9 @@
 // rounding shows.  A tile that sees one block only has its row's P and dP at
 // hand, so it takes rowsum(P dP) instead and leaves it for dK and dV, whose
 // kernel runs after this one.
+//
+// Measured as window_dkv.cu: 560 us, tensor pipe 62 % active (blocks of 64 keys
+// in one ring, as there: 881 us; both tiles in one ring of two: 840 us).
 #include "window.cuh"
 
 namespace syn {
