@@ -6,6 +6,7 @@ contiguous heads; outputs are the caller's."""
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import numpy as np
 from torch import float32 as _float32, int64 as _int64
@@ -51,6 +52,10 @@ SIGS = {
 }
 
 _bound = None
+# the same calls with the structures as packed bytes, which cost a small call a third of what
+# structure objects do (a decoding step's calls are bound by the host)
+_pack_rows = struct.Struct("PqqPqqi4x").pack
+assert struct.calcsize("PqqPqqi4x") == ctypes.sizeof(Rows)
 
 
 def lib():
@@ -63,6 +68,13 @@ def lib():
             f.restype, f.argtypes = res, args
         _bound = L
     return L
+
+
+def packed(L, sigs, name):
+    """Function `name` with pointers to structures taken as bytes."""
+    res, args = sigs[name]
+    plain = [a if issubclass(a, ctypes._SimpleCData) else _P for a in args]
+    return ctypes.CFUNCTYPE(res, *plain)((name, L))
 
 
 def _check(status, where):
@@ -94,13 +106,15 @@ def heads_of(name, t, dtype, d, tokens, heads=None):
     """(address, token stride, head stride, heads) of a CUDA tensor [tokens,
     heads, d] of type `dtype` with contiguous heads; None: any number."""
     shape, stride = t.shape, t.stride()
+    if len(shape) == 3 and t.dtype is dtype and t.is_cuda:
+        n, h, e = shape
+        if e == d and (stride[2] == 1 or d == 1) and (tokens is None or n == tokens) and (heads is None or h == heads):
+            return t.data_ptr(), stride[0], stride[1], h
     if t.dtype is not dtype or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor of type {dtype}")
     if len(shape) != 3 or shape[2] != d or (stride[2] != 1 and d > 1):
         raise ValueError(f"{name} must be [tokens, heads, {d}] with contiguous heads")
-    if (tokens is not None and shape[0] != tokens) or (heads is not None and shape[1] != heads):
-        raise ValueError(f"{name} must have {tokens} rows of {heads} heads")
-    return t.data_ptr(), stride[0], stride[1], shape[1]
+    raise ValueError(f"{name} must have {tokens} rows of {heads} heads")
 
 
 def check_vector(name, t, dtype, n):
@@ -117,6 +131,8 @@ class RopePlan:
         self._h = _P()
         self.cfg = make_cfg(**cfg)
         self.dtype, self._d = torch_dtype(cfg.get("dtype", "bf16")), self.cfg.d
+        self._rope, self._norm, self._back = (packed(self._L, SIGS, n) for n in ("syn_rope", "syn_qk_norm_rope",
+                                                                                 "syn_rope_backward"))
         _check(self._L.syn_rope_plan_create(ctypes.byref(self._h), ctypes.byref(self.cfg)), "syn_rope_plan_create")
 
     def close(self):
@@ -148,7 +164,7 @@ class RopePlan:
         d, dtype = self._d, self.dtype
         p, xt, xh, heads = heads_of(name, x, dtype, d, tokens)
         q, yt, yh, _ = heads_of(name + "_out", y, dtype, d, None if slots else tokens, heads)
-        return Rows(p, xt, xh, q, yt, yh, heads)
+        return _pack_rows(p, xt, xh, q, yt, yh, heads)
 
     def _forward(self, q, q_out, wq, k, k_out, wk, eps, v, v_out, positions, pos0, slots, stream, norm):
         first = q if q is not None else k if k is not None else v
@@ -163,11 +179,11 @@ class RopePlan:
             slot = check_vector("slots", slots, _int64, n)
             n_slots = min((o.shape[0] for t, o in ((k, k_out), (v, v_out)) if t is not None), default=0)
         if not norm:
-            _check(self._L.syn_rope(self._h, rq, rk, rv, pos, pos0, slot, n_slots, n, syn._stream(stream)), "syn_rope")
+            _check(self._rope(self._h, rq, rk, rv, pos, pos0, slot, n_slots, n, syn._stream(stream)), "syn_rope")
             return
         a = None if wq is None else check_vector("wq", wq, self.dtype, self._d)
         b = None if wk is None else check_vector("wk", wk, self.dtype, self._d)
-        _check(self._L.syn_qk_norm_rope(self._h, rq, a, rk, b, eps, rv, pos, pos0, slot, n_slots, n, syn._stream(stream)),
+        _check(self._norm(self._h, rq, a, rk, b, eps, rv, pos, pos0, slot, n_slots, n, syn._stream(stream)),
                "syn_qk_norm_rope")
 
     def rotate(self, q, q_out, k=None, k_out=None, v=None, v_out=None, positions=None, pos0=0, slots=None, stream=None):
@@ -186,7 +202,7 @@ class RopePlan:
             raise ValueError("one of dq_out and dk_out is needed")
         n = first.shape[0]
         pos = None if positions is None else check_vector("positions", positions, _int64, n)
-        _check(self._L.syn_rope_backward(self._h, self._rows("dq_out", dq_out, dq, n), self._rows("dk_out", dk_out, dk, n),
+        _check(self._back(self._h, self._rows("dq_out", dq_out, dq, n), self._rows("dk_out", dk_out, dk, n),
                                          pos, pos0, n, syn._stream(stream)), "syn_rope_backward")
 
     def _grad(self, name, x, dy, dx, w, dw, n):

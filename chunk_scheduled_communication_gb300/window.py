@@ -6,12 +6,13 @@ caller's."""
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import numpy as np
 from torch import float32 as _float32, int32 as _int32
 
 from . import syn
-from .rope import DTYPES, check_vector, heads_of, torch_dtype
+from .rope import DTYPES, check_vector, heads_of, packed, torch_dtype
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -63,6 +64,8 @@ SIGS = {
 }
 
 _bound = None
+# the decoding step's structures as packed bytes (see rope.packed)
+_pack_rows, _pack_cache = struct.Struct("Pqq").pack, struct.Struct("Pqqq").pack
 
 
 def lib():
@@ -180,6 +183,7 @@ class DecodePlan:
         c.dtype, c.max_seqs, c.H_q, c.H_kv, c.d = DTYPES[dtype], max_seqs, H_q, H_kv, d
         c.window, c.sinks, c.page_size, c.scale = window, sinks, page_size, scale
         self.cfg, self.dtype, self._page = c, torch_dtype(dtype), (page_size, H_kv, d)
+        self._decode = packed(self._L, SIGS, "syn_window_decode")
         _check(self._L.syn_decode_plan_create(ctypes.byref(self._h), ctypes.byref(c)), "syn_decode_plan_create")
 
     def close(self):
@@ -204,14 +208,15 @@ class DecodePlan:
         if t.dtype is not self.dtype or not t.is_cuda or len(shape) != 4 or shape[1:] != self._page or stride[3] != 1:
             raise ValueError(f"{name} must be a CUDA tensor [pages, {c.page_size}, {c.H_kv}, {c.d}] of type {self.dtype} "
                              "with contiguous heads")
-        return Cache(t.data_ptr(), stride[0], stride[1], stride[2])
+        return _pack_cache(t.data_ptr(), stride[0], stride[1], stride[2])
 
     def run(self, q, k_cache, v_cache, seq_lens, O, lse=None, page_table=None, stream=None):
         """O of each sequence's last token q[s] over its seq_lens[s] cached tokens.
         page_table: int32 [sequences, pages of a sequence]; None: sequence s is page s."""
         c, n = self.cfg, q.shape[0]
         d, heads = c.d, c.H_q
-        qr, out = _rows("q", q, self.dtype, d, n, heads), _rows("O", O, self.dtype, d, n, heads)
+        qr = _pack_rows(*heads_of("q", q, self.dtype, d, n, heads)[:3])
+        out = _pack_rows(*heads_of("O", O, self.dtype, d, n, heads)[:3])
         k, v = self._cache("k_cache", k_cache), self._cache("v_cache", v_cache)
         pages = k_cache.shape[0]
         if v_cache.shape[0] != pages:
@@ -223,7 +228,7 @@ class DecodePlan:
                     not page_table.is_contiguous():
                 raise ValueError(f"page_table must be a contiguous CUDA tensor [{n}, pages] of int32")
             table, stride = page_table.data_ptr(), shape[1]
-        _check(self._L.syn_window_decode(self._h, qr, k, v, table, stride, pages, lens, n, out, _lse(lse, n, heads),
+        _check(self._decode(self._h, qr, k, v, table, stride, pages, lens, n, out, _lse(lse, n, heads),
                                          syn._stream(stream)), "syn_window_decode")
 
     def sync(self, stream=None) -> int:
