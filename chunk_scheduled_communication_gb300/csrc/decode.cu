@@ -15,10 +15,12 @@
 // ranges' order.
 //
 // Measured on one GB300 (bf16, 32/8 heads of 128): 128 sequences at window 4096,
-// 2.15 GB of visible rows, 355 us, 6.05 TB/s, 0.89 of the measured copy rate
-// (two stages and three CTAs an SM; three and two 419 us, six and one 802 us);
-// three sequences at window 1024 12.5 to 13.5 us, a chain of dependent loads
-// (length, page, row), the join through memory and the launch.
+// 2.15 GB of visible rows, 351 to 355 us, 6.1 TB/s, 0.90 of the measured copy rate
+// (two stages and three CTAs an SM; three and two 419 us, six and one 802 us; the
+// rows of the join that no query head has written too 358 us); three sequences
+// at window 1024 12.4 us, a chain of dependent loads (length, page, row; the
+// query and the second tile's page beside it, else 13.4 us), the join through
+// memory and the launch (a join through the memory of a cluster's CTAs 12.4 us too).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -50,7 +52,8 @@ struct DecParams {
     int64_t q_seq, q_head, o_seq, o_head;
     int64_t k_page, k_token, k_head, v_page, v_token, v_head;
     const int32_t *table, *lens;
-    int64_t table_stride, n_pages, cap;  // cap: keys a sequence's table can name
+    int64_t table_stride, n_pages;
+    int32_t cap;                    // keys a sequence's table can name
     int32_t page_size, page_shift;  // page_shift: log2(page_size), -1: not a power of two
     int32_t window, sinks, H_q, H_kv, G, hgroups, splits;
     float scale_log2;
@@ -110,17 +113,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) window_decode_kernel(co
     const int hk = slot % p.H_kv, s = slot / p.H_kv;
     const int h0 = hk * p.G + hg * kRowsM, rows = min(kRowsM, p.G - hg * kRowsM);
 
-    int len = p.lens[s];
-    if (len < 0) {
-        if (threadIdx.x == 0) atomicCAS(p.err, 0, SYN_ERR_BOUNDS);
-        len = 0;
-    }
-    // visible keys as indexes 0 .. n_vis - 1: the sinks below w_lo, then [w_lo, len)
-    const int w_lo = max(len - p.window, 0), s_end = min(p.sinks, w_lo);
-    const int n_vis = s_end + len - w_lo;
-    const int tiles = (n_vis + kTileKeys - 1) / kTileKeys, per = (tiles + p.splits - 1) / p.splits;
-    const int t0 = min(split * per, tiles), t1 = min(t0 + per, tiles);
-
+    int len = p.lens[s];  // (used after the query's loads are under way)
     uint32_t qf[D / 16][4];
     {
         const uint16_t *q = static_cast<const uint16_t *>(p.q) + (int64_t)s * p.q_seq;
@@ -143,6 +136,17 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) window_decode_kernel(co
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
     }
+    if (len < 0 || len > p.cap) {
+        if (threadIdx.x == 0) atomicCAS(p.err, 0, SYN_ERR_BOUNDS);
+        len = max(len, 0);
+    }
+    // visible keys as indexes 0 .. n_vis - 1: the sinks below w_lo, then [w_lo, len),
+    // both without the keys past the table (so that no length makes a CTA walk them)
+    const int w_lo = max(len - p.window, 0), s_end = min(min(p.sinks, w_lo), p.cap);
+    const int n_vis = s_end + max(min(len, p.cap) - w_lo, 0);
+    const int tiles = (n_vis + kTileKeys - 1) / kTileKeys, per = (tiles + p.splits - 1) / p.splits;
+    const int t0 = min(split * per, tiles), t1 = min(t0 + per, tiles);
+
     // thread: row `r` of a tile's keys (threads 0-63) or values (64-127)
     const int r = (int)threadIdx.x & 63;
     const bool is_v = threadIdx.x >= 64;
@@ -155,17 +159,16 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) window_decode_kernel(co
         return i >= n_vis ? -1 : i < s_end ? i : w_lo + (i - s_end);
     };
     auto page_of = [&](int j) { return p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size; };
-    // the page that holds a key: -1 no key, -2 out of range
+    // the page that holds a key, -1 where there is none (a table's entry may be any number)
     auto lookup = [&](int tile) -> int {
         const int j = tile < t1 ? key_of(tile) : -1;
         if (j < 0) return -1;
-        if (j >= p.cap) return -2;
         return table != nullptr ? table[page_of(j)] : s;
     };
     auto load = [&](int tile, int st, int page) {
         uint8_t *dst = sm + L::RING + (st * 2 + (is_v ? 1 : 0)) * L::kTile + r * L::kRow;
         bool real = page >= 0 && page < p.n_pages;
-        if (!real && page != -1) atomicCAS(p.err, 0, SYN_ERR_BOUNDS);
+        if (!real && key_of(tile) >= 0) atomicCAS(p.err, 0, SYN_ERR_BOUNDS);
         if (!is_v) valid[st * kTileKeys + r] = real;
         if (real) {
             const int j = key_of(tile), at = j - page_of(j) * p.page_size;
@@ -188,7 +191,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) window_decode_kernel(co
             }
         return true;
     };
-    int page = lookup(t0);
+    int page = lookup(t0), ahead = lookup(t0 + 1);
     __syncthreads();  // the barriers are initialised
 
     float o[D / 8][4];
@@ -198,10 +201,9 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) window_decode_kernel(co
         for (int x = 0; x < 4; ++x) o[n][x] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g and g + 8
 
-    for (int x = 0; x < kDecStages - 1; ++x) {
-        if (t0 + x < t1) load(t0 + x, x, page);
-        page = lookup(t0 + x + 1);
-    }
+    static_assert(kDecStages == 2, "one tile ahead");
+    if (t0 < t1) load(t0, 0, page);
+    page = ahead;
     for (int t = t0; t < t1; ++t) {
         const int st = (t - t0) % kDecStages;
         if (t > t0) __syncthreads();  // the stage read last is free
@@ -294,6 +296,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) window_decode_kernel(co
 #pragma unroll
         for (int w = 0; w < 4; ++w) top = fmaxf(top, mm[w * kRowsM + row]);
         const float f = m[r] == -INFINITY ? 1.f : ex2(m[r] - top);  // (no key: O is 0, or NaN from NaN scores)
+        if (row >= rows) continue;  // (a row that no query head has)
 #pragma unroll
         for (int n = 0; n < D / 8; ++n)
             *reinterpret_cast<float2 *>(os + (warp * kRowsM + row) * D + n * 8 + t4 * 2) =
@@ -526,7 +529,9 @@ int syn_window_decode(syn_decode_plan_t pl, const syn_window_rows_t *q, const sy
     p.table = page_table;
     p.table_stride = table_stride;
     p.n_pages = n_pages;
-    p.cap = (page_table != nullptr ? table_stride : 1) * c.page_size;
+    // (no more than the indexes of a tile that starts below it reach in 32 bits)
+    const int64_t pages = page_table != nullptr ? std::min<int64_t>(table_stride, (int64_t)1 << 31) : 1;
+    p.cap = (int32_t)std::min<int64_t>(pages * c.page_size, 0x7fffffff - kTileKeys);
     p.lens = seq_lens;
     p.page_size = c.page_size;
     p.window = (int32_t)c.window;

@@ -16,7 +16,7 @@
 // with the norm, 16384 tokens 67.4 us, 4.98 TB/s (0.73: the rows' shuffle trees
 // and 64 registers a thread leave four blocks an SM to hide the loads); its
 // gradient 98.7 us, 5.10 TB/s (0.75: 127 registers, 16 warps an SM).  A call on
-// a few tokens takes 4-5 us on the device and 7.5-9 us with its host side.
+// a few tokens takes 4-5 us on the device and 7-8.3 us with its host side.
 //
 // The angle of position p and frequency f is p * f mod 2 pi.  f / 2 pi is kept
 // as a 64-bit fraction of a turn; the 64-bit product with p drops whole turns

@@ -440,3 +440,42 @@ def test_decode_reports_what_is_out_of_range():
             plan.run(torch.cat([q, q]), k, v, torch.cat([lens, lens]), torch.cat([q, q]), page_table=torch.cat([table, table]))
         with pytest.raises(ValueError):
             plan.run(q, k[:, :8], v, lens, out, page_table=table)
+
+
+@pytest.mark.parametrize("w, sinks", [(0, 0), (64, 4)])
+@pytest.mark.parametrize("n", [33, 2**30 + 40, 2**31 - 1])
+def test_decode_lengths_past_the_table(w, sinks, n):
+    # the keys that the table names and the window shows remain, however long the sequence claims to be
+    rng = np.random.default_rng(11)
+    k, v, q = make(rng, (4, 16, 1, 64), "bf16"), make(rng, (4, 16, 1, 64), "bf16"), make(rng, (2, 1, 64), "bf16")
+    table = torch.tensor([[2, 1], [0, 3]], dtype=torch.int32, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty((2, 1), dtype=torch.float32, device="cuda")
+    with window.DecodePlan(max_seqs=2, d=64, window=w, sinks=sinks, page_size=16) as plan:
+        plan.run(q, k, v, torch.tensor([n, 5], dtype=torch.int32, device="cuda"), out, page_table=table, lse=lse)
+        assert plan.sync() == syn.ERR_BOUNDS
+        assert plan.sync() == syn.OK
+    first = max(n - min(w or 2**30, 2**30), 0)
+    seen = [j for j in range(32) if j >= first or j < sinks]
+    if not seen:
+        assert not out[0].any() and lse[0].item() == -np.inf
+        return
+    keys, vals = (f64(x)[[2, 1]].reshape(32, 64)[seen] for x in (k, v))
+    scores = keys @ f64(q)[0, 0] / 8
+    weights = np.exp(scores - scores.max())
+    want = weights @ vals / weights.sum()
+    u = TYPES["bf16"][1]
+    assert (np.abs(f64(out)[0, 0] - want) <= (2 * u + S) * np.abs(vals).max()).all()
+
+
+def test_decode_reports_pages_below_zero():
+    rng = np.random.default_rng(12)
+    k, v, q = make(rng, (2, 16, 1, 64), "bf16"), make(rng, (2, 16, 1, 64), "bf16"), make(rng, (1, 1, 64), "bf16")
+    out, ok = torch.empty_like(q), torch.empty_like(q)
+    with window.DecodePlan(max_seqs=1, d=64, page_size=16) as plan:
+        for page in (-1, -2, -2**31):
+            table = torch.tensor([[1, page]], dtype=torch.int32, device="cuda")
+            plan.run(q, k, v, torch.tensor([20], dtype=torch.int32, device="cuda"), out, page_table=table)
+            assert plan.sync() == syn.ERR_BOUNDS
+            plan.run(q, k, v, torch.tensor([16], dtype=torch.int32, device="cuda"), ok, page_table=table)
+            plan.check()
+            assert torch.equal(out, ok)
