@@ -7,16 +7,18 @@
 // one slot of the row: 2 * VEC elements as two 16-byte vectors that contain
 // both members of each of its VEC pairs, so that the turn needs no exchange
 // between lanes and the norm's sum one shuffle tree over L lanes.  A block
-// takes a few tokens with all their heads: its threads issue the loads of their
+// takes a few tokens with all their heads, of all tensors as one run of rows
+// (tensor by tensor the keys' few rows were a pass of their own: the gradient
+// of 5003 tokens 16.5 against 14.5 us): its threads issue the loads of their
 // first rows, compute the tokens' cosines and sines into shared memory while
-// these are under way, and then walk the rows, tensor by tensor.
+// these are under way, and then walk the rows.
 //
 // Measured on one GB300 (bf16, heads of 128; back-to-back calls): the rotation of
-// 32768 tokens x 40 heads 102.5 us, 6.55 TB/s, 0.97 of the measured copy rate;
-// with the norm, 16384 tokens 67.4 us, 4.98 TB/s (0.73: the rows' shuffle trees
-// and 64 registers a thread leave four blocks an SM to hide the loads); its
-// gradient 98.7 us, 5.10 TB/s (0.75: 127 registers, 16 warps an SM).  A call on
-// a few tokens takes 4-5 us on the device and 7-8.3 us with its host side.
+// 32768 tokens x 40 heads 101 us, 6.65 TB/s, 0.98 of the measured copy rate;
+// with the norm, 16384 tokens 60 us, 5.6 TB/s (0.82: 310 instructions for a
+// warp's four rows fill two thirds of the issue slots); its gradient 96.4 us,
+// 5.2 TB/s (0.77: 127 registers, 16 warps an SM).  A call on a few tokens takes
+// 4-6 us on the device and 7-8.3 us with its host side.
 //
 // The angle of position p and frequency f is p * f mod 2 pi.  f / 2 pi is kept
 // as a 64-bit fraction of a turn; the 64-bit product with p drops whole turns
@@ -41,11 +43,13 @@ namespace rope {
 
 constexpr int kThreads = 256;
 constexpr int kMaxD = 256;
+constexpr int kNormPasses = 5;      // passes of a block with the norm at most
+constexpr int kNormBlocksPerSm = 4;
 constexpr int kRowsPerLane = 4;     // rows whose loads a lane has under way at long inputs
 constexpr int kGradRowsPerLane = 3; // (gradient: of the step ahead)
 constexpr int kGradThreads = 128;
 constexpr int kGradBlocksPerSm = 4; // persistent blocks of the gradient kernel
-constexpr int kTableBytes = 14 * 1024;  // cosines and sines of a block's tokens at most
+constexpr int kTableBytes = 12 * 1024;  // cosines and sines of a block's tokens at most
 
 struct Tensor {
     const void *x, *dy;  // dy: the gradient kernel only
@@ -61,6 +65,7 @@ struct Args {
     Tensor t[3];
     int32_t n_tensors, d, d_rot, interleaved;
     uint32_t n_tokens;
+    uint32_t heads, magic, shift;  // of all tensors together; as Tensor::magic (forward)
     uint32_t tokens_of;    // tokens of a block (forward)
     uint32_t table_tokens; // tokens that half of the table of angles holds (gradient), at least 2
     const int64_t *pos, *slots;
@@ -137,9 +142,8 @@ template <typename T> struct Pack<T, 1> {
 template <int VEC, int L, int NS> struct Slots {
     int o0[NS], o1[NS], f0[NS];
     bool rot[NS], has0[NS], has1[NS];
-    __device__ __forceinline__ void init(const Args &a, bool copy, int sub) {
-        const int d_rot = copy ? 0 : a.d_rot;
-        const int n_rot = d_rot / (2 * VEC);
+    __device__ __forceinline__ void init(const Args &a, int sub) {
+        const int d_rot = a.d_rot, n_rot = d_rot / (2 * VEC);
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
             const int s = sub + n * L;
@@ -205,17 +209,26 @@ __device__ __forceinline__ void stage_row(Pack<T, VEC> *st, const T *row, const 
     }
 }
 
+// The packs that no row fills read as zeros: set once, so that no row needs a
+// choice for each element
+template <int TH, typename T, int VEC, int L, int NS>
+__device__ __forceinline__ void clear_rest(Pack<T, VEC> *st, const Slots<VEC, L, NS> &s) {
+    float zero[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) zero[i] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        if (!s.has0[n]) st[(2 * n) * TH + threadIdx.x].narrow(zero);
+        if (!s.has1[n]) st[(2 * n + 1) * TH + threadIdx.x].narrow(zero);
+    }
+}
+
 template <int TH, typename T, int VEC, int L, int NS>
 __device__ __forceinline__ void widen(float (&e)[NS][2 * VEC], const Pack<T, VEC> *st, const Slots<VEC, L, NS> &s) {
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
         st[(2 * n) * TH + threadIdx.x].widen(e[n]);
         st[(2 * n + 1) * TH + threadIdx.x].widen(e[n] + VEC);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            if (!s.has0[n]) e[n][i] = 0.f;
-            if (!s.has1[n]) e[n][VEC + i] = 0.f;
-        }
     }
 }
 
@@ -319,6 +332,31 @@ __device__ __forceinline__ void load_weight(float (&w)[NS][2 * VEC], const void 
     }
 }
 
+// A lane's weights in shared memory, four of a slot beside the next lane's four
+// (single elements: one), which the warp's groups read at once
+template <int VEC, int L, int NS> struct Weights {
+    static constexpr int W = VEC > 1 ? 4 : 1, N = NS * 2 * VEC * L;
+    static __device__ __forceinline__ float *at(float *p, int sub, int n, int i) {
+        return p + ((n * 2 * VEC + i) / W * L + sub) * W;
+    }
+    static __device__ __forceinline__ void put(float *p, int sub, const float (&w)[NS][2 * VEC]) {
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int i = 0; i < 2 * VEC; i += W)
+                if constexpr (W == 4) *reinterpret_cast<float4 *>(at(p, sub, n, i)) = make_float4(w[n][i], w[n][i + 1], w[n][i + 2], w[n][i + 3]);
+                else *at(p, sub, n, i) = w[n][i];
+    }
+    static __device__ __forceinline__ void get(float (&w)[NS][2 * VEC], float *p, int sub) {
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int i = 0; i < 2 * VEC; i += W)
+                if constexpr (W == 4) *reinterpret_cast<float4 *>(&w[n][i]) = *reinterpret_cast<float4 *>(at(p, sub, n, i));
+                else w[n][i] = *at(p, sub, n, i);
+    }
+};
+
 // sum of squares of the lane's elements (an even number)
 template <int NS, int E> __device__ __forceinline__ float squares(const float (&e)[NS][E]) {
     uint64_t q = f2(0.f, 0.f);
@@ -338,69 +376,88 @@ template <typename T, int VEC, int NS, int U> __host__ __device__ constexpr int 
 }
 
 // The forward of both operators (and, with sign -1, the gradient of the
-// rotation): a block takes a.tokens_of tokens.  U: rows of a group that are
-// under way together, each lane's in its own slots of shared memory, so that
-// they cost no registers.
+// rotation): a block takes a.tokens_of tokens and walks their heads, those of
+// all tensors of a token one after another.  U: rows of a group that are under
+// way together, each lane's in its own slots of shared memory, so that they
+// cost no registers.  Each lane computes the place of one of its warp's rows.
 template <typename T, int VEC, int L, int NS, int U, bool NORM>
-__global__ void __launch_bounds__(kThreads, NORM ? 4 : 5) rope_kernel(const __grid_constant__ Args a) {
-    constexpr int G = kThreads / L;
+__global__ void __launch_bounds__(kThreads, NORM ? kNormBlocksPerSm : 5) rope_kernel(const __grid_constant__ Args a) {
+    constexpr uint32_t G = kThreads / L, GW = 32 / L;
+    static_assert(GW * U <= 32, "a lane computes one row's place");
     __shared__ Pack<T, VEC> staged[U][2 * NS * kThreads];
+    // weights: widened into shared memory where a lane has many rows (60.4 against
+    // 62.7 us at 16384 tokens), read as they are for one
+    constexpr bool kShared = NORM && U > 1;
+    __shared__ __align__(16) float weights[kShared ? 3 : 1][kShared ? Weights<VEC, L, NS>::N : 1];
+    static_assert(sizeof(staged) + sizeof(weights) + kTableBytes <= 48 * 1024, "what a launch may use unasked");
     extern __shared__ __align__(16) float table[];
     const int sub = (int)threadIdx.x % L;
-    const uint32_t grp = threadIdx.x / L;
     const uint32_t mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << ((threadIdx.x & 31u) & ~(uint32_t)(L - 1));
+    const uint32_t lane = threadIdx.x & 31u, in_warp = lane / L;  // the group's place in its warp
     const uint32_t tok0 = blockIdx.x * a.tokens_of, n_tok = min(a.tokens_of, a.n_tokens - tok0);
-    bool filled = false;
-    for (int x = 0; x < a.n_tensors; ++x) {
-        const Tensor &t = a.t[x];
-        const bool copy = t.copy, norm = NORM && t.norm, scatter = t.scatter;
-        const uint32_t heads = (uint32_t)t.heads, magic = t.magic, shift = t.shift, rows = n_tok * heads;
-        const T *src = static_cast<const T *>(t.x) + (int64_t)tok0 * t.xt;
-        T *dst = static_cast<T *>(t.y);
-        const int64_t xt = t.xt, xh = t.xh, yt = t.yt, yh = t.yh;
-        Slots<VEC, L, NS> s;
-        s.init(a, copy, sub);
-        for (uint32_t r0 = grp; r0 - grp < rows; r0 += G * U) {
-            uint32_t tok[U];
+    const uint32_t rows = n_tok * a.heads, h0 = (uint32_t)a.t[0].heads, h1 = h0 + (uint32_t)a.t[1].heads;
+    // (a copied row's elements go the same ways as a rotated one's)
+    Slots<VEC, L, NS> s;
+    s.init(a, sub);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t r = r0 + u * G;
-                tok[u] = divide(r, magic, shift);
-                if (r < rows) stage_row<kThreads>(staged[u], src + (int64_t)tok[u] * xt + (int64_t)(r - tok[u] * heads) * xh, s);
+    for (int u = 0; u < U; ++u) clear_rest<kThreads>(staged[u], s);
+    for (uint32_t r0 = 0; r0 < rows; r0 += G * U) {
+        const uint32_t mine = r0 + lane / GW * G + threadIdx.x / 32 * GW + lane % GW;
+        const bool real = lane < GW * U && mine < rows;
+        const uint32_t my_tok = real ? divide(mine, a.magic, a.shift) : 0u;
+        uint32_t my_head = real ? mine - my_tok * a.heads : 0u;
+        const uint32_t my_x = (my_head >= h0) + (my_head >= h1);
+        my_head -= my_x == 0 ? 0 : my_x == 1 ? h0 : h1;
+        const Tensor &my = a.t[my_x];
+        int64_t my_to = (int64_t)tok0 + my_tok;
+        const T *my_src = static_cast<const T *>(my.x) + my_to * my.xt + (int64_t)my_head * my.xh;
+        const bool scatter = my.scatter;
+        if (scatter && real) my_to = a.slots[my_to];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const T *src = reinterpret_cast<const T *>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(my_src), u * GW + in_warp));
+            if (r0 + u * G + threadIdx.x / L < rows) stage_row<kThreads>(staged[u], src, s);
+        }
+        stage_commit();
+        if (r0 == 0) {
+            fill_table<kThreads>(table, a, tok0, n_tok);
+            const uint32_t grp = threadIdx.x / L;  // (a group a tensor: kThreads / L >= 8 of them)
+            if (kShared && grp < (uint32_t)a.n_tensors && a.t[grp].norm) {
+                float w[NS][2 * VEC];
+                load_weight<T>(w, a.t[grp].w, s);
+                Weights<VEC, L, NS>::put(weights[grp], sub, w);
             }
-            stage_commit();
-            if (!filled) {
-                fill_table<kThreads>(table, a, tok0, n_tok);
-                __syncthreads();
-                filled = true;
+            __syncthreads();
+        }
+        const bool kept = real && (!scatter || (my_to >= 0 && my_to < a.n_slots));
+        T *my_dst = static_cast<T *>(my.y) + my_to * my.yt + (int64_t)my_head * my.yh;
+        const uint32_t my_row = kept ? my_tok << 2 | my_x : ~0u;
+        stage_wait<0>();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t row = __shfl_sync(0xffffffffu, my_row, u * GW + in_warp);
+            T *dst = reinterpret_cast<T *>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(my_dst), u * GW + in_warp));
+            if (row == ~0u) continue;
+            const Tensor &t = a.t[row & 3u];
+            float e[NS][2 * VEC];
+            widen<kThreads>(e, staged[u], s);
+            if (NORM && t.norm) {
+                const float inv = rsqrtf(group_sum<L>(squares(e), mask) * a.inv_d + a.eps);
+                float w[NS][2 * VEC];  // (read for each row: kept, it costs a block an SM)
+                if constexpr (kShared) Weights<VEC, L, NS>::get(w, weights[row & 3u], sub);
+                else load_weight<T>(w, t.w, s);
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2 * VEC; i += 2)
+                        unf2(mul2(mul2(at2(e[n], i), f2(inv, inv)), at2(w[n], i)), e[n][i], e[n][i + 1]);
             }
-            stage_wait<0>();
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t r = r0 + u * G;
-                if (r >= rows) break;
-                int64_t to = (int64_t)tok0 + tok[u];
-                if (scatter) {
-                    to = a.slots[to];
-                    if (to < 0 || to >= a.n_slots) continue;
-                }
-                float e[NS][2 * VEC];
-                widen<kThreads>(e, staged[u], s);
-                if (norm) {
-                    const float inv = rsqrtf(group_sum<L>(squares(e), mask) * a.inv_d + a.eps);
-                    float w[NS][2 * VEC];  // (read for each row, from L1: kept, it costs a block an SM)
-                    load_weight<T>(w, t.w, s);
-#pragma unroll
-                    for (int n = 0; n < NS; ++n)
-#pragma unroll
-                        for (int i = 0; i < 2 * VEC; i += 2)
-                            unf2(mul2(mul2(at2(e[n], i), f2(inv, inv)), at2(w[n], i)), e[n][i], e[n][i + 1]);
-                }
+            if (!t.copy) {
                 float cs[NS][VEC], sn[NS][VEC];
-                read_table(cs, sn, table, a, tok[u], s);
+                read_table(cs, sn, table, a, row >> 2, s);
                 turn(e, cs, sn, a, s);
-                store_row(dst + to * yt + (int64_t)(r - tok[u] * heads) * yh, e, s);
             }
+            store_row(dst, e, s);
         }
     }
 }
@@ -423,7 +480,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm) norm_grad_kern
     const uint32_t grp = threadIdx.x / L;
     const uint32_t mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << ((threadIdx.x & 31u) & ~(uint32_t)(L - 1));
     Slots<VEC, L, NS> s;
-    s.init(a, false, sub);
+    s.init(a, sub);
     for (int x = 0; x < a.n_tensors; ++x) {
         const Tensor &t = a.t[x];
         const uint32_t heads = (uint32_t)t.heads, magic = t.magic, shift = t.shift;
@@ -434,6 +491,8 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm) norm_grad_kern
         T *dst = static_cast<T *>(t.y);
         float w[NS][2 * VEC], acc[NS][2 * VEC];
         load_weight<T>(w, t.w, s);
+#pragma unroll
+        for (int k = 0; k < 4 * U; ++k) clear_rest<kGradThreads>(staged + k * kSlots, s);
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -621,10 +680,24 @@ uint32_t tokens_for(int64_t rows, int64_t heads, int d_rot, int bytes) {
     return (uint32_t)std::max<int64_t>(1, std::min<int64_t>(rows / heads, bytes / (4 * std::max(d_rot, 1))));
 }
 
-template <typename T, int VEC, int L, int NS, int U, bool NORM> int launch_forward(Args &a, cudaStream_t st) {
-    int most = 1;
-    for (int x = 0; x < a.n_tensors; ++x) most = std::max(most, a.t[x].heads);
-    a.tokens_of = U > 1 ? tokens_for(kThreads / L * U, most, a.d_rot, kTableBytes) : 1;
+template <typename T, int VEC, int L, int NS, int U, bool NORM> int launch_forward(Args &a, int num_sms, cudaStream_t st) {
+    constexpr int kPass = kThreads / L * U;  // rows of a block's pass
+    a.tokens_of = U > 1 ? tokens_for(kPass * (NORM ? kNormPasses : 1), a.heads, a.d_rot, kTableBytes) : 1;
+    // With the norm a pass costs its instructions too: as many tokens as give the
+    // fewest rounds of resident blocks, a round costing its passes and half a one
+    // (one pass always 65.2 us, up to five 60.4 at 16384 tokens; without the norm
+    // one pass 101.4, three 104.0 us at 32768).
+    if (NORM && U > 1) {
+        const uint64_t slots = (uint64_t)num_sms * kNormBlocksPerSm;
+        uint64_t least = ~0ull;
+        for (uint32_t t = a.tokens_of, best = t; t >= 1; a.tokens_of = best, --t) {
+            const uint64_t rounds = ((a.n_tokens + t - 1) / t + slots - 1) / slots, passes = ((uint64_t)t * a.heads + kPass - 1) / kPass;
+            if (rounds * (2 * passes + 1) < least) {
+                least = rounds * (2 * passes + 1);
+                best = t;
+            }
+        }
+    }
     const unsigned grid = (a.n_tokens + a.tokens_of - 1) / a.tokens_of;
     rope_kernel<T, VEC, L, NS, U, NORM><<<grid, kThreads, (size_t)a.tokens_of * (size_t)a.d_rot * 4, st>>>(a);
     ROPE_CK(cudaGetLastError());
@@ -654,8 +727,8 @@ template <typename T, int VEC, int L, int NS> int launch(syn_rope_plan_s *pl, Ar
     for (int x = 0; x < a.n_tensors; ++x) rows += (int64_t)a.n_tokens * a.t[x].heads;
     const bool many = rows >= (int64_t)pl->num_sms * 4 * G * kMany;
     if (kind == kTurn)
-        return many ? launch_forward<T, VEC, L, NS, kMany, false>(a, st) : launch_forward<T, VEC, L, NS, 1, false>(a, st);
-    return many ? launch_forward<T, VEC, L, NS, kMany, true>(a, st) : launch_forward<T, VEC, L, NS, 1, true>(a, st);
+        return many ? launch_forward<T, VEC, L, NS, kMany, false>(a, pl->num_sms, st) : launch_forward<T, VEC, L, NS, 1, false>(a, pl->num_sms, st);
+    return many ? launch_forward<T, VEC, L, NS, kMany, true>(a, pl->num_sms, st) : launch_forward<T, VEC, L, NS, 1, true>(a, pl->num_sms, st);
 }
 
 // A lane's slot is two 16-byte vectors where every row, stride and both parts
@@ -666,13 +739,23 @@ template <typename T> int dispatch(syn_rope_plan_s *pl, Args &a, Kind kind, bool
     const int slots = a.d / (2 * V);
     if (slots <= 4) return launch<T, V, 4, 1>(pl, a, kind, st, grid);
     if (slots <= 8) return launch<T, V, 8, 1>(pl, a, kind, st, grid);
-    if (slots <= 16) return launch<T, V, 16, 1>(pl, a, kind, st, grid);
-    return launch<T, V, 32, 1>(pl, a, kind, st, grid);
+    if constexpr (sizeof(T) == 4)
+        if (slots > 16) return launch<T, V, 32, 1>(pl, a, kind, st, grid);
+    return launch<T, V, 16, 1>(pl, a, kind, st, grid);
+}
+
+// r / n for r < 2^31 as r * magic >> shift
+void divisor(int n, uint32_t &magic, uint32_t &shift) {
+    uint32_t bits = 0;
+    while (((int64_t)1 << bits) < n) ++bits;
+    shift = 31 + bits;
+    magic = (uint32_t)((((uint64_t)1 << shift) + (uint64_t)n - 1) / (uint64_t)n);
 }
 
 int run(syn_rope_plan_s *pl, Args &a, Kind kind, cudaStream_t st, int &grid) {
     const syn_rope_cfg_t &c = pl->cfg;
     grid = 0;
+    a.heads = 0;
     a.d = c.d;
     a.d_rot = c.d_rot;
     a.interleaved = c.layout == SYN_ROPE_INTERLEAVED;
@@ -690,14 +773,12 @@ int run(syn_rope_plan_s *pl, Args &a, Kind kind, cudaStream_t st, int &grid) {
         rows += (int64_t)a.n_tokens * t.heads;
     }
     if (rows == 0) return SYN_OK;
-    for (int x = 0; x < a.n_tensors; ++x) {  // rows stay below 2^31
-        Tensor &t = a.t[x];
-        uint32_t bits = 0;
-        while (((int64_t)1 << bits) < t.heads) ++bits;
-        t.shift = 31 + bits;
-        t.magic = (uint32_t)((((uint64_t)1 << t.shift) + (uint64_t)t.heads - 1) / (uint64_t)t.heads);
-    }
     if (rows >= (int64_t)1 << 31) return host_fail(SYN_ERR_UNSUPPORTED, "2^31 or more rows in one call");
+    for (int x = 0; x < a.n_tensors; ++x) {
+        divisor(a.t[x].heads, a.t[x].magic, a.t[x].shift);
+        a.heads += (uint32_t)a.t[x].heads;
+    }
+    divisor((int)a.heads, a.magic, a.shift);
     if (c.dtype == SYN_DTYPE_BF16) return dispatch<__nv_bfloat16>(pl, a, kind, vec, st, grid);
     if (c.dtype == SYN_DTYPE_F16) return dispatch<__half>(pl, a, kind, vec, st, grid);
     return dispatch<float>(pl, a, kind, vec, st, grid);

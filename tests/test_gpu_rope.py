@@ -234,6 +234,37 @@ def test_packed_projection_into_cache_slots():
     assert torch.equal(kc, want_k) and torch.equal(vc, want_v)
 
 
+@pytest.mark.parametrize("t, hq, hkv, d, rot, layout, dtype", [
+    (40001, 1, 1, 256, 256, "half", "bf16"), (20011, 1, 1, 256, 64, "interleaved", "fp32"),
+    (9001, 5, 2, 128, 64, "half", "bf16"), (18007, 3, 2, 80, 48, "interleaved", "fp16"), (701, 1, 1, 77, 34, "half", "bf16")])
+def test_many_rows_of_few_heads_into_slots(t, hq, hkv, d, rot, layout, dtype):
+    """Several rows a lane, blocks of many tokens, rows of three tensors in one
+    pass; every third slot is none."""
+    rng = np.random.default_rng(t)
+    q, k, v = make(rng, (t, hq, d), dtype), make(rng, (t, hkv, d), dtype), make(rng, (t, hkv, d), dtype)
+    wq, wk = make(rng, (d,), dtype), make(rng, (d,), dtype)
+    to = rng.permutation(t)
+    to[::3] = rng.choice([-1, t, 2 ** 40], len(to[::3]))
+    slots = torch.from_numpy(to).cuda()
+    qo, ko, vo = torch.full_like(q, 7), torch.full_like(k, 7), torch.full_like(v, 7)
+    f, factor = frequencies(rot, 10000.0, None)
+    pos, eps = np.arange(t) + 31, 1e-6
+    kept = (to >= 0) & (to < t)
+    rest = np.setdiff1d(np.arange(t), to[kept])
+    with rope.RopePlan(d=d, d_rot=rot, layout=layout, dtype=dtype) as plan:
+        for norm in (True, False):
+            if norm:
+                plan.norm_rotate(q, qo, wq, k, ko, wk, v, vo, pos0=31, slots=slots, eps=eps)
+            else:
+                plan.rotate(q, qo, k, ko, v, vo, pos0=31, slots=slots)
+            for x, w, y, rows in ((q, wq, qo, slice(None)), (k, wk, ko, kept)):
+                h = norm_ref(f64(x)[rows], f64(w), eps)[0] if norm else f64(x)[rows]
+                ref, mag = turn(h, pos[rows], rot, layout, f, factor)
+                near(y if x is q else y[slots[torch.from_numpy(kept).cuda()]], ref, (64 if norm else 16) * U * mag)
+            assert torch.equal(vo[slots[torch.from_numpy(kept).cuda()]], v[torch.from_numpy(kept).cuda()])
+            assert (ko[torch.from_numpy(rest).cuda()] == 7).all() and (vo[torch.from_numpy(rest).cuda()] == 7).all()
+
+
 def test_strides_and_streams():
     """Head-major tensors, an unaligned view, and a stream of the caller's."""
     rng = np.random.default_rng(6)
