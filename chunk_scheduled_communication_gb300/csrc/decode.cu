@@ -15,12 +15,12 @@
 // ranges' order.
 //
 // Measured on one GB300 (bf16, 32/8 heads of 128): 128 sequences at window 4096,
-// 2.15 GB of visible rows, 351 to 355 us, 6.1 TB/s, 0.90 of the measured copy rate
+// 2.15 GB of visible rows, 346 to 348 us, 6.2 TB/s, 0.91 of the measured copy rate
 // (two stages and three CTAs an SM; three and two 419 us, six and one 802 us; the
 // rows of the join that no query head has written too 358 us); three sequences
-// at window 1024 12.4 us, a chain of dependent loads (length, page, row; the
-// query and the second tile's page beside it, else 13.4 us), the join through
-// memory and the launch (a join through the memory of a cluster's CTAs 12.4 us too).
+// at window 1024 10.3 us, a chain of dependent loads (length, page, row; the
+// query and the second tile's page beside it: 1 us less) and the join through
+// memory (one through the shared memory of a cluster's CTAs: no change).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -113,6 +113,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) window_decode_kernel(co
     const int hk = slot % p.H_kv, s = slot / p.H_kv;
     const int h0 = hk * p.G + hg * kRowsM, rows = min(kRowsM, p.G - hg * kRowsM);
 
+    ptx::grid_wait();
     int len = p.lens[s];  // (used after the query's loads are under way)
     uint32_t qf[D / 16][4];
     {
@@ -381,8 +382,7 @@ template <int D, bool BF16> cudaError_t dec_prepare() {
     return cudaFuncSetAttribute(window_decode_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecLay<D>::BYTES);
 }
 template <int D, bool BF16> cudaError_t dec_launch(int grid, const DecParams &p, cudaStream_t st) {
-    window_decode_kernel<D, BF16><<<grid, kDecThreads, DecLay<D>::BYTES, st>>>(p);
-    return cudaGetLastError();
+    return launch_early(window_decode_kernel<D, BF16>, grid, kDecThreads, DecLay<D>::BYTES, st, p);
 }
 
 }  // namespace

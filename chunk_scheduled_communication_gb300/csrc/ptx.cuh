@@ -39,6 +39,11 @@ __device__ __forceinline__ void grid_dep_launch_dependents() {
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
+// Kernels launched beside the end of the one before (launch_early, window.cuh):
+// before grid_wait they read nothing that an earlier kernel may have written and
+// write nothing that it may read.  Every thread passes it, so that the end of a
+// grid implies the ends of those before it.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void fence_mbar_init() {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }

@@ -14,11 +14,11 @@
 // these are under way, and then walk the rows.
 //
 // Measured on one GB300 (bf16, heads of 128; back-to-back calls): the rotation of
-// 32768 tokens x 40 heads 101 us, 6.65 TB/s, 0.98 of the measured copy rate;
-// with the norm, 16384 tokens 60 us, 5.6 TB/s (0.82: 310 instructions for a
-// warp's four rows fill two thirds of the issue slots); its gradient 96.4 us,
-// 5.2 TB/s (0.77: 127 registers, 16 warps an SM).  A call on a few tokens takes
-// 4-6 us on the device and 7-8.3 us with its host side.
+// 32768 tokens x 40 heads 98.5 us, 6.8 TB/s, the measured copy rate;
+// with the norm, 16384 tokens 57.6 us, 5.8 TB/s (0.86: 310 instructions for a
+// warp's four rows fill two thirds of the issue slots); its gradient 91.8 us,
+// 5.5 TB/s (0.81: 127 registers, 16 warps an SM).  A call on a few tokens takes
+// 2.7-3.3 us on the device and 7-8.3 us with its host side.
 //
 // The angle of position p and frequency f is p * f mod 2 pi.  f / 2 pi is kept
 // as a 64-bit fraction of a turn; the 64-bit product with p drops whole turns
@@ -481,6 +481,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm) norm_grad_kern
     const uint32_t mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << ((threadIdx.x & 31u) & ~(uint32_t)(L - 1));
     Slots<VEC, L, NS> s;
     s.init(a, sub);
+    ptx::grid_wait();
     for (int x = 0; x < a.n_tensors; ++x) {
         const Tensor &t = a.t[x];
         const uint32_t heads = (uint32_t)t.heads, magic = t.magic, shift = t.shift;
@@ -586,6 +587,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *partial, int
     __shared__ float sums[32][33];
     const int j = (int)(blockIdx.x * 32 + threadIdx.x);
     float *dw = blockIdx.y == 0 ? dw0 : dw1;
+    ptx::grid_wait();
     if (dw == nullptr) return;
     float v = 0.f;
     if (j < d)
@@ -699,8 +701,8 @@ template <typename T, int VEC, int L, int NS, int U, bool NORM> int launch_forwa
         }
     }
     const unsigned grid = (a.n_tokens + a.tokens_of - 1) / a.tokens_of;
-    rope_kernel<T, VEC, L, NS, U, NORM><<<grid, kThreads, (size_t)a.tokens_of * (size_t)a.d_rot * 4, st>>>(a);
-    ROPE_CK(cudaGetLastError());
+    ROPE_CK((window::launch_early(rope_kernel<T, VEC, L, NS, U, NORM>, grid, kThreads,
+                                  (size_t)a.tokens_of * (size_t)a.d_rot * 4, st, a)));
     return SYN_OK;
 }
 
@@ -718,8 +720,7 @@ template <typename T, int VEC, int L, int NS> int launch(syn_rope_plan_s *pl, Ar
         grid = (int)std::min<int64_t>(blocks, (int64_t)pl->num_sms * kGradBlocksPerSm);
         const size_t smem = (size_t)grad_stage_bytes<T, VEC, NS, U>() + (size_t)a.table_tokens * (size_t)a.d_rot * 8;
         ROPE_CK(cudaFuncSetAttribute(norm_grad_kernel<T, VEC, L, NS, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-        norm_grad_kernel<T, VEC, L, NS, U><<<grid, kGradThreads, smem, st>>>(a);
-        ROPE_CK(cudaGetLastError());
+        ROPE_CK((window::launch_early(norm_grad_kernel<T, VEC, L, NS, U>, grid, kGradThreads, smem, st, a)));
         return SYN_OK;
     }
     // several rows a lane once that still leaves every SM a few blocks
@@ -989,9 +990,8 @@ int syn_qk_norm_rope_backward(syn_rope_plan_t pl, const syn_rope_grad_t *q, cons
     int grid = 0;
     rc = run(pl, a, kNormGrad, st, grid);
     if (rc != SYN_OK || a.n_tensors == 0 || (dw[0] == nullptr && dw[1] == nullptr)) return rc;
-    norm_dw_kernel<<<dim3((unsigned)(pl->cfg.d + 31) / 32, (unsigned)a.n_tensors), dim3(32, 32), 0, st>>>(
-        pl->d_partial, grid, pl->cfg.d, dw[0], dw[1]);
-    ROPE_CK(cudaGetLastError());
+    ROPE_CK((window::launch_early(norm_dw_kernel, dim3((unsigned)(pl->cfg.d + 31) / 32, (unsigned)a.n_tensors), dim3(32, 32), 0,
+                                  st, pl->d_partial, grid, pl->cfg.d, dw[0], dw[1])));
     return SYN_OK;
 }
 

@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
         ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
         ptx::tmem_relinquish();
     }
+    ptx::grid_wait();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -373,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
 constexpr int kPrepRows = 4;
 template <bool BF16, int D> __global__ void __launch_bounds__(256) window_prep_kernel(const __grid_constant__ PrepParams p) {
     const PrepTile t = p.tiles[blockIdx.x];
+    ptx::grid_wait();
     const int sub = (int)threadIdx.x & 7, grp = (int)threadIdx.x >> 3;
     const uint32_t mask = 0xffu << (threadIdx.x & 24u);
     uint4 x[kPrepRows][D / 64], y[kPrepRows][D / 64];
@@ -430,6 +432,7 @@ template <bool BF16, int D> __global__ void __launch_bounds__(256) window_prep_k
 // dK, dV tiles that were summed in parts: the parts in their fixed order
 template <bool BF16> __global__ void __launch_bounds__(256) window_sum_kernel(const __grid_constant__ SumParams p) {
     const SumItem it = p.items[blockIdx.x];
+    ptx::grid_wait();
     const int per = p.d / 8, rows = 256 / per;  // rows of a block: one vector of eight a thread
     const int r = (int)blockIdx.z * rows + (int)threadIdx.x / per, k = (int)threadIdx.x % per * 8;
     if (r < it.n_rows) {
@@ -454,8 +457,7 @@ template <bool BF16> __global__ void __launch_bounds__(256) window_sum_kernel(co
 }
 
 template <int D, bool BF16> cudaError_t launch(int grid, const BwdParams &p, const BwdMaps &m, cudaStream_t st) {
-    window_dkv_kernel<D, BF16><<<grid, kThreads, Lay<D>::BYTES, st>>>(p, m);
-    return cudaGetLastError();
+    return launch_early(window_dkv_kernel<D, BF16>, grid, kThreads, Lay<D>::BYTES, st, p, m);
 }
 template <int D, bool BF16> cudaError_t prepare() {
     return cudaFuncSetAttribute(window_dkv_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::BYTES);
@@ -475,21 +477,15 @@ cudaError_t dkv_launch(int d, bool bf16, int grid, const BwdParams &p, const Bwd
 
 cudaError_t bwd_prep_launch(bool bf16, int n_tiles, const PrepParams &p, cudaStream_t st) {
     const dim3 grid((unsigned)n_tiles, (unsigned)((64 * p.H_q + 32 * kPrepRows - 1) / (32 * kPrepRows)));
-    if (p.d == 64) {
-        if (bf16) window_prep_kernel<true, 64><<<grid, 256, 0, st>>>(p);
-        else window_prep_kernel<false, 64><<<grid, 256, 0, st>>>(p);
-    } else {
-        if (bf16) window_prep_kernel<true, 128><<<grid, 256, 0, st>>>(p);
-        else window_prep_kernel<false, 128><<<grid, 256, 0, st>>>(p);
-    }
-    return cudaGetLastError();
+    return launch_early(p.d == 64 ? bf16 ? window_prep_kernel<true, 64> : window_prep_kernel<false, 64>
+                        : bf16    ? window_prep_kernel<true, 128>
+                                  : window_prep_kernel<false, 128>,
+                        grid, 256, 0, st, p);
 }
 
 cudaError_t bwd_sum_launch(bool bf16, int n_items, const SumParams &p, cudaStream_t st) {
     const dim3 grid((unsigned)n_items, 2, (unsigned)(kBX * p.d / 8 / 256));
-    if (bf16) window_sum_kernel<true><<<grid, 256, 0, st>>>(p);
-    else window_sum_kernel<false><<<grid, 256, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_early(bf16 ? window_sum_kernel<true> : window_sum_kernel<false>, grid, 256, 0, st, p);
 }
 
 }  // namespace window

@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_con
         ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
         ptx::tmem_relinquish();
     }
+    ptx::grid_wait();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -404,8 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_con
 }
 
 template <int D, bool BF16> cudaError_t launch(int grid, const BwdParams &p, const BwdMaps &m, cudaStream_t st) {
-    window_dq_kernel<D, BF16><<<grid, kThreads, Lay<D>::BYTES, st>>>(p, m);
-    return cudaGetLastError();
+    return launch_early(window_dq_kernel<D, BF16>, grid, kThreads, Lay<D>::BYTES, st, p, m);
 }
 template <int D, bool BF16> cudaError_t prepare() {
     return cudaFuncSetAttribute(window_dq_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::BYTES);

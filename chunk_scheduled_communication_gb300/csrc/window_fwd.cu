@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
         ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
         ptx::tmem_relinquish();
     }
+    ptx::grid_wait();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -466,8 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
 
 template <int D, bool BF16>
 cudaError_t launch(int grid, const FwdParams &p, const FwdMaps &m, cudaStream_t st) {
-    window_fwd_kernel<D, BF16><<<grid, kThreads, Lay<D>::BYTES, st>>>(p, m);
-    return cudaGetLastError();
+    return launch_early(window_fwd_kernel<D, BF16>, grid, kThreads, Lay<D>::BYTES, st, p, m);
 }
 template <int D, bool BF16> cudaError_t prepare() {
     return cudaFuncSetAttribute(window_fwd_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::BYTES);

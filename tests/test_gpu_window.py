@@ -479,3 +479,69 @@ def test_decode_reports_pages_below_zero():
             plan.run(q, k, v, torch.tensor([16], dtype=torch.int32, device="cuda"), ok, page_table=table)
             plan.check()
             assert torch.equal(out, ok)
+
+
+def test_dependent_calls_back_to_back_and_in_a_graph():
+    """Each call reads what the one before wrote and overwrites what it read;
+    the same bits with a pause after each call, without, and replayed."""
+    from chunk_scheduled_communication_gb300 import rope
+
+    rng = np.random.default_rng(21)
+    lens, hq, hkv, d, page = [70, 1, 333], 4, 2, 64, 16
+    n = sum(lens)
+    x0 = [make(rng, (n, h, d), "bf16") for h in (hq, hkv, hkv)]
+    do, w = make(rng, (n, hq, d), "bf16"), make(rng, (d,), "bf16")
+    x = [t.clone() for t in x0]
+    out, lse = torch.empty_like(x[0]), torch.empty((n, hq), device="cuda")
+    g = [torch.empty_like(t) for t in x]
+    k_rows, v_rows = (torch.zeros((n + page, hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    slots = torch.arange(n, device="cuda")
+    pages = -(-n // page)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None].contiguous()
+    length, one = torch.tensor([n], dtype=torch.int32, device="cuda"), torch.empty((1, hq, d), dtype=torch.bfloat16, device="cuda")
+    with rope.RopePlan(d=d) as turn, window.WindowPlan(lens, H_q=hq, H_kv=hkv, d=d, window=50, sinks=2, backward=True) as plan, \
+            window.DecodePlan(max_seqs=1, H_q=hq, H_kv=hkv, d=d, window=50, sinks=2, page_size=page) as step:
+        def calls(pause):
+            for i in range(3):
+                turn.norm_rotate(x[0], x[0], w, x[1], x[1], w)  # in place
+                pause()
+                plan.forward(*x, out, lse=lse)
+                pause()
+                plan.backward(do, *x, out, lse, *g)
+                pause()
+                turn.rotate(g[0], x[0], g[1], k_rows, g[2], v_rows, slots=slots)
+                pause()
+                step.run(x[0][-1:], k_rows[:pages * page].view(pages, page, hkv, d), v_rows[:pages * page].view(pages, page, hkv, d),
+                         length, one, page_table=table)
+                pause()
+                turn.rotate(k_rows[:n], x[1], v_rows[:n], x[2])
+                pause()
+
+        def start():
+            for a, b in zip(x, x0):
+                a.copy_(b)
+
+        def result():
+            torch.cuda.synchronize()
+            got = [t.clone() for t in (*x, out, lse, *g, k_rows, v_rows, one)]
+            return got
+
+        start()
+        calls(torch.cuda.synchronize)
+        want = result()
+        assert all(t.isfinite().all() for t in want)
+        for _ in range(20):
+            start()
+            calls(lambda: None)
+            assert all(torch.equal(a, b) for a, b in zip(result(), want))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            start()
+            calls(lambda: None)
+        for _ in range(3):
+            for t in x:
+                t.zero_()
+            graph.replay()
+            assert all(torch.equal(a, b) for a, b in zip(result(), want))
+        plan.check()
+        step.check()
