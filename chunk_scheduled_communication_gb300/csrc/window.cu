@@ -188,6 +188,72 @@ bool query_blocks(int64_t j0, int64_t j1, int64_t ql, int64_t off, int64_t windo
     return true;
 }
 
+// A key tile's `G` heads x `blocks` cut into head ranges x block ranges of at
+// most `most` blocks (>= 1): the fewest parts, and of those the most even
+void cut(int G, int64_t blocks, int64_t most, int &by_head, int64_t &by_block) {
+    int64_t parts = INT64_MAX, largest = INT64_MAX;
+    for (int h = 1; h <= G; ++h) {
+        const int64_t heads = (G + h - 1) / h, fit = most / heads;
+        if (fit < 1) continue;
+        const int64_t b = (blocks + fit - 1) / fit, size = heads * ((blocks + b - 1) / b);
+        if (h * b < parts || (h * b == parts && size < largest)) {
+            parts = h * b;
+            largest = size;
+            by_head = h;
+            by_block = b;
+        }
+    }
+}
+
+// What an item of dK, dV costs beside its blocks, in blocks (its K and V, the
+// start and end of its pipeline); a part's fp32 sums cost 1 / kPartsPerBlock of a
+// CTA's block each (written and read again, 256 KB).
+constexpr int kItemCost = 4, kPartsPerBlock = 28;
+
+// The largest part of a key tile, in blocks.  Where there are few tiles a CTA,
+// the one of a ladder around a CTA's share that gives the least cost of the
+// busiest CTA and the sums; the costs alone are dealt out.  (Sequences of 1024,
+// 517, 63 and 1531 tokens, 14/2 heads, window 300, against parts of 16 blocks:
+// busiest CTA 32 -> 25 blocks, 184 -> 132 parts, gradient 77.1 -> 69.6 us; four
+// of 2048, causal, 32/8 heads 464.8 -> 429.2; one of 257, 16/4 heads 33.4 -> 28.5;
+// the plan takes 0.1 to 0.4 ms longer.)  Where there are many the order costliest first evens them out.
+int64_t part_size(const std::vector<int64_t> &tiles, int G, int num_sms) {
+    int64_t blocks = 0;
+    for (int64_t t : tiles) blocks += t * G;
+    const int64_t share = std::max<int64_t>(blocks / num_sms, 1);
+    if (tiles.size() > 4 * (size_t)num_sms) return std::max<int64_t>(share / 2, 16);
+    int64_t best = share, least = INT64_MAX;
+    std::vector<int> cost;
+    for (int64_t most = std::max<int64_t>(share / 6, 4); most <= 2 * share + 24; most += std::max<int64_t>(most / 5, 2)) {
+        cost.clear();
+        int64_t parts = 0;
+        for (int64_t t : tiles) {
+            int h;
+            int64_t b;
+            cut(G, t, most, h, b);
+            for (int x = 0; x < h; ++x)
+                for (int64_t y = 0; y < b; ++y)
+                    cost.push_back((int)((G * (x + 1) / h - G * x / h) * (t * (y + 1) / b - t * y / b)) + kItemCost);
+            parts += h * b > 1 ? h * b : 0;
+        }
+        std::sort(cost.begin(), cost.end(), std::greater<int>());
+        std::vector<int64_t> load((size_t)std::min<int64_t>(num_sms, (int64_t)cost.size()), 0);
+        std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> q(std::greater<int64_t>(), std::move(load));
+        int64_t busiest = 0;
+        for (int x : cost) {
+            const int64_t v = q.top() + x;
+            q.pop();
+            q.push(v);
+            busiest = std::max(busiest, v);
+        }
+        if (busiest * kPartsPerBlock + parts < least) {
+            least = busiest * kPartsPerBlock + parts;
+            best = most;
+        }
+    }
+    return best;
+}
+
 void build_keys(Lists &l, const syn_window_cfg_t &c, int64_t window, int64_t q0, int64_t k0, int64_t ql, int64_t kl,
                 int64_t most) {
     const int G = c.H_q / c.H_kv;
@@ -206,10 +272,9 @@ void build_keys(Lists &l, const syn_window_cfg_t &c, int64_t window, int64_t q0,
                 l.sums.push_back(sum);  // seen by no query: zero gradients
                 continue;
             }
-            const int64_t cost = G * (b1 - b0);
-            const int64_t n = (cost + most - 1) / most;                     // parts wanted
-            const int by_head = (int)std::min<int64_t>(G, n);               // head ranges
-            const int64_t by_block = std::min<int64_t>(b1 - b0, (n + by_head - 1) / by_head);  // block ranges
+            int by_head;
+            int64_t by_block;
+            cut(G, b1 - b0, most, by_head, by_block);
             const int64_t parts = by_head * by_block;
             for (int x = 0; x < by_head; ++x)
                 for (int64_t y = 0; y < by_block; ++y) {
@@ -229,7 +294,7 @@ void build_keys(Lists &l, const syn_window_cfg_t &c, int64_t window, int64_t q0,
                     it.pad_row0 = (int32_t)l.pad_rows;
                     it.part = parts > 1 ? l.n_parts++ : -1;
                     l.keys.push_back(it);
-                    l.key_cost.push_back((it.h1 - it.h0) * (it.b1 - it.b0) + 4);
+                    l.key_cost.push_back((it.h1 - it.h0) * (it.b1 - it.b0) + kItemCost);
                 }
             if (parts > 1) {
                 sum.n_parts = (int32_t)parts;
@@ -349,16 +414,14 @@ int syn_window_plan_create(syn_window_plan_t *out, const syn_window_cfg_t *cfg, 
         PL_CK(dq_prepare(c.d, pl->bf16));
     }
 
-    // parts of at most `most` blocks: a third of what one CTA gets in all
-    const int G = c.H_q / c.H_kv;
-    int64_t blocks = 0;
+    std::vector<int64_t> tiles;  // query blocks of each tile of keys
     for (int s = 0; c.backward && s < n_seqs; ++s)
         for (int64_t j0 = 0; j0 < k_lens[s]; j0 += 128) {
             int64_t b0, b1;
             if (query_blocks(j0, std::min(j0 + 128, k_lens[s]), q_lens[s], k_lens[s] - q_lens[s], c.window, c.sinks, b0, b1))
-                blocks += (b1 - b0) * G * c.H_kv;
+                tiles.insert(tiles.end(), (size_t)c.H_kv, b1 - b0);
         }
-    const int64_t most = std::max<int64_t>(16, blocks / (3 * (int64_t)pl->num_sms));
+    const int64_t most = part_size(tiles, c.H_q / c.H_kv, pl->num_sms);
     Lists l;
     int64_t q0 = 0, k0 = 0, pairs = 0;
     for (int s = 0; s < n_seqs; ++s) {
