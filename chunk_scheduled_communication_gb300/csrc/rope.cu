@@ -401,6 +401,9 @@ __global__ void __launch_bounds__(kThreads, NORM ? kNormBlocksPerSm : 5) rope_ke
     s.init(a, sub);
 #pragma unroll
     for (int u = 0; u < U; ++u) clear_rest<kThreads>(staged[u], s);
+    // rows, positions, slots and weights may be the previous kernel's, and so may
+    // readers of the rows written here
+    ptx::grid_wait();
     for (uint32_t r0 = 0; r0 < rows; r0 += G * U) {
         const uint32_t mine = r0 + lane / GW * G + threadIdx.x / 32 * GW + lane % GW;
         const bool real = lane < GW * U && mine < rows;

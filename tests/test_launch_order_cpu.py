@@ -1,0 +1,55 @@
+"""Every kernel that may start beside the end of the stream's kernel before it
+waits for that kernel (checked in the sources, without a GPU)."""
+import glob
+import os
+import re
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "chunk_scheduled_communication_gb300", "csrc")
+
+
+def closing(text, at, pair):
+    """Index of the bracket that closes the one at `at`."""
+    depth = 0
+    for i in range(at, len(text)):
+        depth += (text[i] == pair[0]) - (text[i] == pair[1])
+        if depth == 0:
+            return i
+    raise AssertionError("unbalanced source")
+
+
+def sources():
+    for path in sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))):
+        yield re.sub(r"//[^\n]*|/\*.*?\*/", "", open(path).read(), flags=re.S)
+
+
+def early_kernels():
+    names = set()
+    for text in sources():
+        for m in re.finditer(r"(?<!\w)launch_early\(", text):
+            call = text[m.start():closing(text, m.end() - 1, "()")]
+            if "cudaError_t launch_early" not in text[max(m.start() - 12, 0):m.end()]:
+                names |= set(re.findall(r"\b(\w+_kernel)\b", call))
+    return names
+
+
+def body(name):
+    found = []
+    for text in sources():
+        for m in re.finditer(r"__global__[^;{]*?\b" + name + r"\(", text):
+            begin = text.index("{", closing(text, m.end() - 1, "()"))
+            found.append(text[begin:closing(text, begin, "{}")])
+    assert len(found) == 1, (name, len(found))
+    return found[0]
+
+
+def test_every_early_kernel_waits_in_every_thread():
+    names = early_kernels()
+    assert {"rope_kernel", "norm_grad_kernel", "window_fwd_kernel", "window_decode_kernel"} <= names
+    for name in sorted(names):
+        text = body(name)
+        assert text.count("ptx::grid_wait();") == 1, name
+        before = re.sub(r"\[&\]\([^)]*\)\s*\{[^{}]*\}", "", text[:text.index("ptx::grid_wait();")])  # without lambdas
+        # unconditional: no block is open at the wait, nothing returns before it
+        assert before.count("{") - before.count("}") == 1, name
+        assert not re.search(r"\breturn\b", before), name
