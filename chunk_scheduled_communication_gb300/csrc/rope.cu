@@ -72,7 +72,7 @@ struct Args {
     int64_t pos0, n_slots;
     const uint64_t *step;  // [d_rot / 2] turns per position, as 64-bit fractions
     float factor, sign, eps, inv_d;
-    float *partial;        // [grid][2][kMaxD] weight-gradient sums
+    float *partial;        // [grid][2][kMaxD] weight-gradient sums (nullptr: not wanted)
 };
 
 template <typename T> struct Num;
@@ -567,6 +567,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm) norm_grad_kern
         }
         stage_wait<0>();
         __syncthreads();  // every lane has read its staged rows
+        if (a.partial == nullptr) continue;
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -766,7 +767,6 @@ int run(syn_rope_plan_s *pl, Args &a, Kind kind, cudaStream_t st, int &grid) {
     a.step = pl->d_step;
     a.factor = (float)pl->factor;
     a.inv_d = 1.f / (float)c.d;
-    a.partial = pl->d_partial;
     const int size = elem_size(c.dtype);
     bool vec = c.d % (32 / size) == 0 && c.d_rot % (32 / size) == 0;
     int64_t rows = 0;
@@ -990,9 +990,12 @@ int syn_qk_norm_rope_backward(syn_rope_plan_t pl, const syn_rope_grad_t *q, cons
         if (p != nullptr) ROPE_CK(cudaMemsetAsync(p, 0, (size_t)pl->cfg.d * sizeof(float), st));
     a.sign = -1.f;
     a.eps = eps;
+    // the plan's workspace belongs to the one call that wants weight gradients
+    const bool sums = dw[0] != nullptr || dw[1] != nullptr;
+    a.partial = sums ? pl->d_partial : nullptr;
     int grid = 0;
     rc = run(pl, a, kNormGrad, st, grid);
-    if (rc != SYN_OK || a.n_tensors == 0 || (dw[0] == nullptr && dw[1] == nullptr)) return rc;
+    if (rc != SYN_OK || a.n_tensors == 0 || !sums) return rc;
     ROPE_CK((window::launch_early(norm_dw_kernel, dim3((unsigned)(pl->cfg.d + 31) / 32, (unsigned)a.n_tensors), dim3(32, 32), 0,
                                   st, pl->d_partial, grid, pl->cfg.d, dw[0], dw[1])));
     return SYN_OK;

@@ -338,3 +338,26 @@ def test_refused_calls():
         assert L.syn_rope(plan._h, None, None, None, None, 0, None, 0, -1, None) == syn.ERR_INVALID
         r = rope.Rows(0, 1, 1, 0, 1, 1, 2)
         assert L.syn_rope(plan._h, r, None, None, None, 0, None, 0, 4, None) == syn.ERR_INVALID
+
+
+def test_gradient_without_weights_beside_one_with_them():
+    """Calls that want no weight gradients run beside one of the same plan that does, on another stream."""
+    rng = np.random.default_rng(12)
+    t, h, d = 3000, 4, 128
+    x, dy, w = make(rng, (t, h, d), "bf16"), make(rng, (t, h, d), "bf16"), make(rng, (d,), "bf16")
+    x2, dy2 = make(rng, (t, h, d), "bf16", 3.0), make(rng, (t, h, d), "bf16", 3.0)
+    dx, dx2, ref, ref2 = (torch.empty_like(x) for _ in range(4))
+    dw, want = torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    with rope.RopePlan() as plan:
+        plan.norm_rotate_backward(x, dy, ref, w, want)
+        plan.norm_rotate_backward(x2, dy2, ref2, w, None)
+        torch.cuda.synchronize()
+        for _ in range(200):
+            for _ in range(3):
+                plan.norm_rotate_backward(x2, dy2, dx2, w, None, stream=b)
+            plan.norm_rotate_backward(x, dy, dx, w, dw, stream=a)
+            for _ in range(3):
+                plan.norm_rotate_backward(x2, dy2, dx2, w, None, stream=b)
+            torch.cuda.synchronize()
+            assert torch.equal(dw, want) and torch.equal(dx, ref) and torch.equal(dx2, ref2)
