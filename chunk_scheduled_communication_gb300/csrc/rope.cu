@@ -723,7 +723,6 @@ template <typename T, int VEC, int L, int NS> int launch(syn_rope_plan_s *pl, Ar
         }
         grid = (int)std::min<int64_t>(blocks, (int64_t)pl->num_sms * kGradBlocksPerSm);
         const size_t smem = (size_t)grad_stage_bytes<T, VEC, NS, U>() + (size_t)a.table_tokens * (size_t)a.d_rot * 8;
-        ROPE_CK(cudaFuncSetAttribute(norm_grad_kernel<T, VEC, L, NS, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
         ROPE_CK((window::launch_early(norm_grad_kernel<T, VEC, L, NS, U>, grid, kGradThreads, smem, st, a)));
         return SYN_OK;
     }
@@ -734,6 +733,25 @@ template <typename T, int VEC, int L, int NS> int launch(syn_rope_plan_s *pl, Ar
     if (kind == kTurn)
         return many ? launch_forward<T, VEC, L, NS, kMany, false>(a, pl->num_sms, st) : launch_forward<T, VEC, L, NS, 1, false>(a, pl->num_sms, st);
     return many ? launch_forward<T, VEC, L, NS, kMany, true>(a, pl->num_sms, st) : launch_forward<T, VEC, L, NS, 1, true>(a, pl->num_sms, st);
+}
+
+// The gradient kernels may use as much shared memory as any call needs: set once
+// here, since the limit is the context's, and a call that set its own need could
+// lower it under another host thread's launch.
+template <typename T, int VEC, int L, int NS> cudaError_t prepare() {
+    constexpr int U = VEC == 1 ? 1 : kGradRowsPerLane;
+    return cudaFuncSetAttribute(norm_grad_kernel<T, VEC, L, NS, U>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                grad_stage_bytes<T, VEC, NS, U>() + 2 * kTableBytes);
+}
+template <typename T> cudaError_t prepare_all() {
+    constexpr int V = 16 / (int)sizeof(T);
+    cudaError_t e = prepare<T, 1, 32, 4>();
+    if (e == cudaSuccess) e = prepare<T, V, 4, 1>();
+    if (e == cudaSuccess) e = prepare<T, V, 8, 1>();
+    if (e == cudaSuccess) e = prepare<T, V, 16, 1>();
+    if constexpr (sizeof(T) == 4)
+        if (e == cudaSuccess) e = prepare<T, V, 32, 1>();
+    return e;
 }
 
 // A lane's slot is two 16-byte vectors where every row, stride and both parts
@@ -895,6 +913,8 @@ int syn_rope_plan_create(syn_rope_plan_t *out, const syn_rope_cfg_t *cfg) {
     for (size_t i = 0; i < step.size(); ++i) step[i] = (uint64_t)std::ldexp(pl->f[i] / (2 * kPi), 64);
     cudaError_t e = cudaGetDevice(&pl->device);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&pl->num_sms, cudaDevAttrMultiProcessorCount, pl->device);
+    if (e == cudaSuccess)
+        e = c.dtype == SYN_DTYPE_BF16 ? prepare_all<__nv_bfloat16>() : c.dtype == SYN_DTYPE_F16 ? prepare_all<__half>() : prepare_all<float>();
     if (e == cudaSuccess) e = cudaMalloc(&pl->d_step, std::max<size_t>(step.size(), 1) * sizeof(uint64_t));
     if (e == cudaSuccess)
         e = cudaMalloc(&pl->d_partial, (size_t)pl->num_sms * kGradBlocksPerSm * 2 * kMaxD * sizeof(float));

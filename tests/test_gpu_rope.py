@@ -361,3 +361,37 @@ def test_gradient_without_weights_beside_one_with_them():
                 plan.norm_rotate_backward(x2, dy2, dx2, w, None, stream=b)
             torch.cuda.synchronize()
             assert torch.equal(dw, want) and torch.equal(dx, ref) and torch.equal(dx2, ref2)
+
+
+def test_gradients_from_two_host_threads():
+    """Two threads, each with a plan of its own, in calls that need different amounts of shared memory."""
+    import threading
+
+    rng = np.random.default_rng(14)
+    failed = []
+
+    def work(x, dy, w, want, gate):
+        dx, st = torch.empty_like(x), torch.cuda.Stream()
+        with rope.RopePlan() as plan:
+            gate.wait()
+            try:
+                for _ in range(3000):
+                    plan.norm_rotate_backward(x, dy, dx, w, None, stream=st)
+                st.synchronize()
+                assert torch.equal(dx, want)
+            except BaseException as e:
+                failed.append(e)
+
+    threads, gate = [], threading.Barrier(2)
+    for heads in (1, 64):  # a step spans many tokens' angles, or few
+        x, dy, w = make(rng, (64 // heads, heads, 128), "bf16"), make(rng, (64 // heads, heads, 128), "bf16"), make(rng, (128,), "bf16")
+        want = torch.empty_like(x)
+        with rope.RopePlan() as plan:
+            plan.norm_rotate_backward(x, dy, want, w, None)
+        threads.append(threading.Thread(target=work, args=(x, dy, w, want, gate)))
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed[0]

@@ -53,3 +53,18 @@ def test_every_early_kernel_waits_in_every_thread():
         # unconditional: no block is open at the wait, nothing returns before it
         assert before.count("{") - before.count("}") == 1, name
         assert not re.search(r"\breturn\b", before), name
+
+
+def test_kernel_attributes_are_set_by_plans_alone():
+    """A kernel's attributes are the context's: a call that set them would change
+    them under another host thread's launch."""
+    seen = 0
+    for text in sources():
+        if "launch_early(" not in text:
+            continue
+        for m in re.finditer(r"cudaFuncSetAttribute\(", text):
+            # the function that the call stands in: the last one at file level before it
+            name = re.findall(r"^(?:template <[^>]*> )?[\w:]+ (\w+)\([^;]*?\) \{", text[:m.start()], flags=re.M)[-1]
+            assert name.endswith("prepare"), name
+            seen += 1
+    assert seen >= 5
