@@ -920,6 +920,8 @@ int syn_rope_plan_create(syn_rope_plan_t *out, const syn_rope_cfg_t *cfg) {
         e = cudaMalloc(&pl->d_partial, (size_t)pl->num_sms * kGradBlocksPerSm * 2 * kMaxD * sizeof(float));
     if (e == cudaSuccess && !step.empty())
         e = cudaMemcpy(pl->d_step, step.data(), step.size() * sizeof(uint64_t), cudaMemcpyHostToDevice);
+    // (the copy may return before it has reached the device, which other streams would not wait for)
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
         syn_rope_plan_destroy(pl);
         return host_fail(SYN_ERR_CUDA, std::string("rope plan: ") + cudaGetErrorString(e));

@@ -395,3 +395,23 @@ def test_gradients_from_two_host_threads():
     for t in threads:
         t.join()
     assert not failed, failed[0]
+
+
+def test_a_new_plan_on_another_stream():
+    """The first call of a plan, on a stream that does not wait for the default one, while that one is busy."""
+    rng = np.random.default_rng(15)
+    x = make(rng, (64, 4, 256), "fp32")
+    y, ref, busy = torch.empty_like(x), torch.empty_like(x), torch.zeros(1 << 26, device="cuda")
+    with rope.RopePlan(d=256, dtype="fp32") as plan:
+        plan.rotate(x, ref, pos0=1000)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    for _ in range(50):
+        y.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            busy.add_(1)
+        with rope.RopePlan(d=256, dtype="fp32") as plan:
+            plan.rotate(x, y, pos0=1000, stream=st)
+            st.synchronize()
+            assert torch.equal(y, ref)

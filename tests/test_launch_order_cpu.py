@@ -68,3 +68,18 @@ def test_kernel_attributes_are_set_by_plans_alone():
             assert name.endswith("prepare"), name
             seen += 1
     assert seen >= 5
+
+
+def test_a_plan_is_on_the_device_when_it_is_made():
+    """What a plan's creation copies and clears has reached the device before the
+    plan is handed out: a stream of the caller's need not wait for the default one."""
+    made = 0
+    for text in sources():
+        for m in re.finditer(r"^int syn_(rope|window|decode)_plan_create\(", text, flags=re.M):
+            begin = text.index("{", closing(text, m.end() - 1, "()"))
+            create = text[begin:closing(text, begin, "{}")]
+            # (the null pointer at the start aside)
+            last = create.rindex("*out = pl;")
+            assert "cudaDeviceSynchronize()" in create[:last], m.group(1)
+            made += 1
+    assert made == 3
