@@ -569,6 +569,7 @@ int syn_decode_sync_status(syn_decode_plan_t pl, void *stream) {
     DEC_CK(cudaMemcpy(&e, pl->d_err, sizeof(e), cudaMemcpyDeviceToHost));
     if (e == 0) return SYN_OK;
     DEC_CK(cudaMemset(pl->d_err, 0, sizeof(e)));
+    DEC_CK(cudaDeviceSynchronize());  // (cleared before a later call, of whatever stream, can report)
     return host_fail(e, "decode: a length, table entry or page out of range; those keys were left out");
 }
 

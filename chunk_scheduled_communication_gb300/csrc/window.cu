@@ -618,6 +618,7 @@ int syn_window_sync_status(syn_window_plan_t pl, void *stream) {
     WIN_CK(cudaMemcpy(e, pl->d_err, sizeof(e), cudaMemcpyDeviceToHost));
     if (e[0] == 0) return SYN_OK;
     WIN_CK(cudaMemset(pl->d_err, 0, sizeof(e)));
+    WIN_CK(cudaDeviceSynchronize());  // (cleared before a later call, of whatever stream, can report)
     return host_fail(e[0], std::string("device error ") + syn_status_string(e[0]) + " at site " + std::to_string(e[1]) +
                                " in CTA " + std::to_string(e[2]) + " (info " + std::to_string(e[3]) + ")");
 }

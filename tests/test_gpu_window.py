@@ -545,3 +545,17 @@ def test_dependent_calls_back_to_back_and_in_a_graph():
             assert all(torch.equal(a, b) for a, b in zip(result(), want))
         plan.check()
         step.check()
+
+
+def test_an_error_after_a_cleared_one_is_reported():
+    rng = np.random.default_rng(16)
+    k, v, q = make(rng, (2, 16, 1, 64), "bf16"), make(rng, (2, 16, 1, 64), "bf16"), make(rng, (1, 1, 64), "bf16")
+    out, table = torch.empty_like(q), torch.tensor([[1, 7]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([20], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with window.DecodePlan(max_seqs=1, d=64, page_size=16) as plan:
+        for _ in range(200):
+            plan.run(q, k, v, lens, out, page_table=table, stream=st)  # page 7 of 2
+            assert plan.sync(st) == syn.ERR_BOUNDS
+        assert plan.sync(st) == syn.OK

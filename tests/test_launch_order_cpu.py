@@ -83,3 +83,14 @@ def test_a_plan_is_on_the_device_when_it_is_made():
             assert "cudaDeviceSynchronize()" in create[:last], m.group(1)
             made += 1
     assert made == 3
+
+
+def test_a_cleared_error_word_is_cleared_before_the_next_call():
+    found = 0
+    for text in sources():
+        for m in re.finditer(r"^int syn_\w*sync_status\(", text, flags=re.M):
+            begin = text.index("{", closing(text, m.end() - 1, "()"))
+            clear = text[begin:closing(text, begin, "{}")]
+            assert "cudaDeviceSynchronize()" in clear[clear.rindex("cudaMemset("):], m.group(0)
+            found += 1
+    assert found >= 4
