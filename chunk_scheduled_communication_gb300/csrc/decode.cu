@@ -45,6 +45,7 @@ constexpr int kDecStages = 2;
 constexpr int kDecCtas = 3;        // resident on an SM
 constexpr int kMaxSplits = 128;
 constexpr int kWaves = 6;          // CTAs wanted per resident slot
+constexpr uint64_t kDrainNs = 1000000000;  // more for copies under way, after a wait past the limit
 constexpr int kMinTiles = 1;       // tiles of a range at least, where there are that many
 
 struct DecParams {
@@ -181,16 +182,23 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) window_decode_kernel(co
             ptx::mbar_arrive(bar(st));
         }
     };
-    // the rows of the stage landed; bounded
+    // the rows of the stage landed; left by a warp's lanes together.  A wait past
+    // the limit is reported and goes on for kDrainNs, so that no copy is under way
+    // when its memory is used for something else; one past that too is given up.
     auto landed = [&](int st, uint32_t parity) {
-        if (ptx::mbar_try_wait(bar(st), parity)) return true;
-        const uint64_t begin = ptx::globaltimer();
-        while (!ptx::mbar_try_wait(bar(st), parity))
-            if (ptx::globaltimer() - begin > p.timeout_ns) {
+        bool ok = poll_bar(bar(st), parity);
+        if (!ok) {
+            const uint64_t begin = ptx::globaltimer();
+            uint64_t limit = p.timeout_ns;
+            while (!(ok = poll_bar(bar(st), parity))) {
+                if (ptx::globaltimer() - begin <= limit) continue;
+                if (limit != p.timeout_ns) break;
                 atomicCAS(p.err, 0, SYN_ERR_TIMEOUT);
-                return false;
+                limit += kDrainNs;
             }
-        return true;
+        }
+        __syncwarp();
+        return ok;
     };
     int page = lookup(t0), ahead = lookup(t0 + 1);
     __syncthreads();  // the barriers are initialised
@@ -205,12 +213,13 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) window_decode_kernel(co
     static_assert(kDecStages == 2, "one tile ahead");
     if (t0 < t1) load(t0, 0, page);
     page = ahead;
+    bool lost = false;  // a wait was given up: nothing more is loaded or waited for
     for (int t = t0; t < t1; ++t) {
         const int st = (t - t0) % kDecStages;
         if (t > t0) __syncthreads();  // the stage read last is free
-        if (t + kDecStages - 1 < t1) load(t + kDecStages - 1, (t - t0 + kDecStages - 1) % kDecStages, page);
+        if (t + kDecStages - 1 < t1 && !lost) load(t + kDecStages - 1, (t - t0 + kDecStages - 1) % kDecStages, page);
         page = lookup(t + kDecStages);
-        landed(st, (uint32_t)((t - t0) / kDecStages) & 1u);
+        if (!lost) lost = !landed(st, (uint32_t)((t - t0) / kDecStages) & 1u);
         const uint32_t kd = sbase + (uint32_t)(L::RING + st * 2 * L::kTile), vd = kd + L::kTile;
         float sc[2][4] = {};
         {
@@ -570,7 +579,8 @@ int syn_decode_sync_status(syn_decode_plan_t pl, void *stream) {
     if (e == 0) return SYN_OK;
     DEC_CK(cudaMemset(pl->d_err, 0, sizeof(e)));
     DEC_CK(cudaDeviceSynchronize());  // (cleared before a later call, of whatever stream, can report)
-    return host_fail(e, "decode: a length, table entry or page out of range; those keys were left out");
+    return host_fail(e, e == SYN_ERR_TIMEOUT ? "decode: rows of the cache did not arrive within the time limit"
+                                             : "decode: a length, table entry or page out of range; those keys were left out");
 }
 
 }  // extern "C"

@@ -559,3 +559,28 @@ def test_an_error_after_a_cleared_one_is_reported():
             plan.run(q, k, v, lens, out, page_table=table, stream=st)  # page 7 of 2
             assert plan.sync(st) == syn.ERR_BOUNDS
         assert plan.sync(st) == syn.OK
+
+
+def test_decode_waits_that_run_out(monkeypatch):
+    """A limit that no wait is sure to meet: the call ends, says what happened, and the next one is right."""
+    rng = np.random.default_rng(17)
+    b, page, d = 64, 64, 128
+    pages = b * 32
+    k, v = (torch.randn((pages, page, 4, d), device="cuda").bfloat16() for _ in range(2))
+    q, out, ref = make(rng, (b, 8, d), "bf16"), *(torch.empty((b, 8, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = torch.from_numpy(rng.permutation(pages).astype(np.int32).reshape(b, 32)).cuda()
+    lens = torch.full((b,), 32 * page, dtype=torch.int32, device="cuda")
+    with window.DecodePlan(max_seqs=b, H_q=8, H_kv=4, window=1024, sinks=4, page_size=page) as plan:
+        plan.run(q, k, v, lens, ref, page_table=table)
+        plan.check()
+        for _ in range(5):
+            monkeypatch.setenv("SYN_TIMEOUT_NS", "1")
+            plan.run(q, k, v, lens, out, page_table=table)
+            status = plan.sync()
+            assert status in (syn.OK, syn.ERR_TIMEOUT)
+            if status == syn.ERR_TIMEOUT:
+                assert b"time limit" in syn.lib().syn_last_error()
+            monkeypatch.delenv("SYN_TIMEOUT_NS")
+            plan.run(q, k, v, lens, out, page_table=table)
+            plan.check()
+            assert torch.equal(out, ref)

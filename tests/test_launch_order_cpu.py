@@ -94,3 +94,16 @@ def test_a_cleared_error_word_is_cleared_before_the_next_call():
             assert "cudaDeviceSynchronize()" in clear[clear.rindex("cudaMemset("):], m.group(0)
             found += 1
     assert found >= 4
+
+
+def test_decode_waits_leave_a_warp_whole_and_a_lost_copy_ends_the_loading():
+    text = next(t for t in sources() if "window_decode_kernel(" in t and "__global__" in t)
+    at = text.index("auto landed")
+    wait = text[at:closing(text, text.index("{", at), "{}")]
+    # the matrix loads and products behind it need converged warps
+    assert wait.count("return") == 1 and "__syncwarp();" in wait[:wait.index("return")]
+    # reported at the limit, then waited for again, with a limit of its own
+    assert wait.index("SYN_ERR_TIMEOUT") < wait.index("limit += kDrainNs")
+    # a barrier whose rows never came is not armed again
+    assert "&& !lost) load(t +" in text and "if (!lost) lost = !landed(" in text
+    assert "SYN_ERR_TIMEOUT ?" in text
