@@ -11,6 +11,8 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <memory>
+#include <new>
 #include <queue>
 #include <string>
 #include <vector>
@@ -49,6 +51,7 @@ namespace {
     } while (0)
 
 constexpr int64_t kMaxLen = (int64_t)1 << 29;  // positions and window sums stay within 32 bits
+constexpr int64_t kMaxItems = (int64_t)1 << 28;  // of a work list (16 GB): its indexes stay within 32 bits
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
@@ -114,6 +117,11 @@ void key_ranges(int64_t p0, int64_t p1, int64_t window, int sinks, int32_t &s_en
     w_lo = (int32_t)lo;
     s_end = (int32_t)std::min<int64_t>(sinks, lo);
     k_end = (int32_t)(p1 + 1);
+}
+
+// Items that build_forward makes of ql queries
+int64_t forward_items(const syn_window_cfg_t &c, int64_t ql) {
+    return c.H_q / c.H_kv % 2 == 0 ? (int64_t)c.H_q / 2 * ceil_div(ql, 128) : (int64_t)c.H_q * ceil_div(ql, 256);
 }
 
 void build_forward(Lists &l, const syn_window_cfg_t &c, int64_t window, int64_t q0, int64_t k0, int64_t ql, int64_t kl) {
@@ -365,7 +373,7 @@ int syn_window_cfg_default(syn_window_cfg_t *c) {
 }
 
 int syn_window_plan_create(syn_window_plan_t *out, const syn_window_cfg_t *cfg, int n_seqs, const int64_t *q_lens,
-                           const int64_t *k_lens) {
+                           const int64_t *k_lens) try {
     if (out == nullptr || cfg == nullptr) return host_fail(SYN_ERR_INVALID, "null argument");
     *out = nullptr;
     syn_window_cfg_t c = *cfg;
@@ -379,30 +387,39 @@ int syn_window_plan_create(syn_window_plan_t *out, const syn_window_cfg_t *cfg, 
     if (c.window < 0 || c.sinks < 0) return host_fail(SYN_ERR_INVALID, "window and sinks must not be negative");
     if (!(c.scale >= 0.f) || !std::isfinite(c.scale)) return host_fail(SYN_ERR_INVALID, "bad scale");
     if (c.backward != 0 && c.backward != 1) return host_fail(SYN_ERR_INVALID, "backward must be 0 or 1");
-    int64_t q_rows = 0, k_rows = 0;
+    int64_t q_rows = 0, k_rows = 0, n_fwd = 0, n_queries = 0, n_keys = 0;
     for (int s = 0; s < n_seqs; ++s) {
         if (q_lens[s] < 0 || k_lens[s] < 0) return host_fail(SYN_ERR_INVALID, "negative length");
         if (q_lens[s] >= kMaxLen || k_lens[s] >= kMaxLen) return host_fail(SYN_ERR_UNSUPPORTED, "length of 2^29 or more");
         q_rows += q_lens[s];
         k_rows += k_lens[s];
+        n_fwd += forward_items(c, q_lens[s]);
+        n_queries += (int64_t)c.H_q * ceil_div(q_lens[s], 128);
+        n_keys += (int64_t)c.H_kv * ceil_div(k_lens[s], 128);
     }
     if (q_rows >= (int64_t)1 << 30 || k_rows >= (int64_t)1 << 30) return host_fail(SYN_ERR_UNSUPPORTED, "2^30 or more rows");
+    if (n_fwd >= kMaxItems || (c.backward && (n_queries >= kMaxItems || n_keys >= kMaxItems)))
+        return host_fail(SYN_ERR_UNSUPPORTED, "2^28 or more tiles");
     if (c.window == 0 || c.window > kNoWindow) c.window = kNoWindow;
     c.sinks = (int)std::min<int64_t>(c.sinks, kMaxLen);
     if (c.scale == 0.f) c.scale = 1.f / std::sqrt((float)c.d);
     if (c.timeout_ns == 0) c.timeout_ns = host_timeout_ns();
+    std::vector<int64_t> tiles;  // query blocks of each tile of keys
+    for (int s = 0; c.backward && s < n_seqs; ++s)
+        for (int64_t j0 = 0; j0 < k_lens[s]; j0 += 128) {
+            int64_t b0, b1;
+            if (query_blocks(j0, std::min(j0 + 128, k_lens[s]), q_lens[s], k_lens[s] - q_lens[s], c.window, c.sinks, b0, b1))
+                tiles.insert(tiles.end(), (size_t)c.H_kv, b1 - b0);
+        }
     int rc = host_load_driver();
     if (rc != SYN_OK) return rc;
 
     syn_window_plan_s *pl = new syn_window_plan_s();
-    auto bail = [&](cudaError_t e) {
-        free_plan(pl);
-        return host_fail(SYN_ERR_CUDA, std::string("window plan: ") + cudaGetErrorString(e));
-    };
-#define PL_CK(call)                              \
-    do {                                         \
-        cudaError_t e__ = (call);                \
-        if (e__ != cudaSuccess) return bail(e__); \
+    std::unique_ptr<syn_window_plan_s, void (*)(syn_window_plan_s *)> unfinished(pl, free_plan);
+#define PL_CK(call)                                                                                                     \
+    do {                                                                                                                \
+        cudaError_t e__ = (call);                                                                                       \
+        if (e__ != cudaSuccess) return host_fail(SYN_ERR_CUDA, std::string("window plan: ") + cudaGetErrorString(e__)); \
     } while (0)
     pl->cfg = c;
     pl->bf16 = c.dtype == SYN_DTYPE_BF16;
@@ -414,13 +431,6 @@ int syn_window_plan_create(syn_window_plan_t *out, const syn_window_cfg_t *cfg, 
         PL_CK(dq_prepare(c.d, pl->bf16));
     }
 
-    std::vector<int64_t> tiles;  // query blocks of each tile of keys
-    for (int s = 0; c.backward && s < n_seqs; ++s)
-        for (int64_t j0 = 0; j0 < k_lens[s]; j0 += 128) {
-            int64_t b0, b1;
-            if (query_blocks(j0, std::min(j0 + 128, k_lens[s]), q_lens[s], k_lens[s] - q_lens[s], c.window, c.sinks, b0, b1))
-                tiles.insert(tiles.end(), (size_t)c.H_kv, b1 - b0);
-        }
     const int64_t most = part_size(tiles, c.H_q / c.H_kv, pl->num_sms);
     Lists l;
     int64_t q0 = 0, k0 = 0, pairs = 0;
@@ -481,8 +491,11 @@ int syn_window_plan_create(syn_window_plan_t *out, const syn_window_cfg_t *cfg, 
     f.k_rows = k_rows;
     f.pairs = pairs;
     f.workspace_bytes = (int64_t)(c.backward ? stats + part : 0);
+    unfinished.release();
     *out = pl;
     return SYN_OK;
+} catch (const std::bad_alloc &) {  // (the lists grow with the lengths)
+    return host_fail(SYN_ERR_UNSUPPORTED, "not enough host memory for the work lists");
 }
 
 int syn_window_plan_destroy(syn_window_plan_t pl) {

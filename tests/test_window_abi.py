@@ -6,6 +6,7 @@ import os
 import re
 import shutil
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -88,4 +89,31 @@ def test_headers_compile_as_plain_c(tmp_path):
         "    syn_window_plan_destroy(wp);\n    syn_rope_plan_destroy(rp);\n    return st;\n}\n")
     r = subprocess.run([gcc, "-std=c11", "-Wall", "-Werror", "-fsyntax-only", "-I", os.path.join(ROOT, "include"), str(src)],
                        capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("lens, kw", [
+    ([1 << 28] * 3, dict(H_q=1024, H_kv=1024)), ([1 << 28] * 3, dict(H_q=1024, H_kv=2)), ([1 << 20] * 1000, dict(H_q=128, H_kv=1)),
+    ([1 << 28] * 3, dict(H_q=48, H_kv=8, backward=1)), ([1] * (1 << 20), dict(H_q=512, H_kv=512))])
+def test_more_tiles_than_a_plan_can_hold(lens, kw):
+    """Refused before the lists are built: 2^28 tiles are 16 GB."""
+    assert create_window(lens, **kw) == syn.ERR_UNSUPPORTED
+    assert b"tiles" in syn.lib().syn_last_error()
+
+
+def test_a_plan_that_host_memory_cannot_hold():
+    """An error of the call, not the end of the process (a child with little memory left)."""
+    code = (
+        "import ctypes, resource, numpy as np\n"
+        "from chunk_scheduled_communication_gb300 import syn, window\n"
+        "c = window.WindowCfg()\n"
+        "window.lib().syn_window_cfg_default(ctypes.byref(c))\n"
+        "c.H_q = c.H_kv = 64\n"
+        "c.backward = 1\n"
+        "n, h = np.array([1 << 28], np.int64), ctypes.c_void_p()\n"
+        "have = int(open('/proc/self/statm').read().split()[0]) * resource.getpagesize()\n"
+        "resource.setrlimit(resource.RLIMIT_AS, (have + (64 << 20), resource.RLIM_INFINITY))\n"
+        "rc = window.lib().syn_window_plan_create(ctypes.byref(h), ctypes.byref(c), 1, n.ctypes.data, n.ctypes.data)\n"
+        "assert rc == syn.ERR_UNSUPPORTED and b'memory' in syn.lib().syn_last_error(), rc\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
     assert r.returncode == 0, r.stderr
