@@ -421,17 +421,18 @@ namespace {
 
 bool al16(const void *x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }
 
-int check_cache(const char *name, const syn_window_cache_t *c) {
+// (a stride of an axis with one entry is never used)
+int check_cache(const char *name, const syn_window_cache_t *c, int64_t pages, int page_size, int heads) {
     if (c == nullptr || c->p == nullptr) return host_fail(SYN_ERR_INVALID, std::string(name) + ": null operand");
     if (!al16(c->p)) return host_fail(SYN_ERR_INVALID, std::string(name) + ": operand not 16-byte aligned");
-    if (c->page % 8 != 0 || c->token % 8 != 0 || c->head % 8 != 0)
+    if ((pages > 1 && c->page % 8 != 0) || (page_size > 1 && c->token % 8 != 0) || (heads > 1 && c->head % 8 != 0))
         return host_fail(SYN_ERR_INVALID, std::string(name) + ": strides must be multiples of 8 elements");
     return SYN_OK;
 }
 
-int check_query(const char *name, const syn_window_rows_t *r) {
+int check_query(const char *name, const syn_window_rows_t *r, int rows, int heads) {
     if (r == nullptr || r->p == nullptr) return host_fail(SYN_ERR_INVALID, std::string(name) + ": null operand");
-    if (!al16(r->p) || r->token % 8 != 0 || r->head % 8 != 0)
+    if (!al16(r->p) || (rows > 1 && r->token % 8 != 0) || (heads > 1 && r->head % 8 != 0))
         return host_fail(SYN_ERR_INVALID, std::string(name) + ": not 16-byte aligned, or strides not multiples of 8 elements");
     return SYN_OK;
 }
@@ -511,8 +512,9 @@ int syn_window_decode(syn_decode_plan_t pl, const syn_window_rows_t *q, const sy
     if (n_seqs < 0 || n_seqs > c.max_seqs) return host_fail(SYN_ERR_INVALID, "n_seqs must be in [0, max_seqs]");
     if (n_seqs == 0) return SYN_OK;
     int rc;
-    if ((rc = check_query("q", q)) != SYN_OK || (rc = check_query("O", O)) != SYN_OK || (rc = check_cache("k", k)) != SYN_OK ||
-        (rc = check_cache("v", v)) != SYN_OK)
+    if ((rc = check_query("q", q, n_seqs, c.H_q)) != SYN_OK || (rc = check_query("O", O, n_seqs, c.H_q)) != SYN_OK ||
+        (rc = check_cache("k", k, n_pages, c.page_size, c.H_kv)) != SYN_OK ||
+        (rc = check_cache("v", v, n_pages, c.page_size, c.H_kv)) != SYN_OK)
         return rc;
     if (seq_lens == nullptr) return host_fail(SYN_ERR_INVALID, "null seq_lens");
     if (n_pages < 0 || n_pages >= (int64_t)1 << 31) return host_fail(SYN_ERR_INVALID, "n_pages must be in [0, 2^31)");

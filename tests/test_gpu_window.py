@@ -584,3 +584,26 @@ def test_decode_waits_that_run_out(monkeypatch):
             plan.run(q, k, v, lens, out, page_table=table)
             plan.check()
             assert torch.equal(out, ref)
+
+
+def test_decode_strides_of_single_entries():
+    """A stride of an axis with one entry is never used, whatever it is."""
+    rng = np.random.default_rng(18)
+    k, v, q = make(rng, (1, 64, 1, 64), "bf16"), make(rng, (1, 64, 1, 64), "bf16"), make(rng, (1, 1, 64), "bf16")
+    k1, v1 = make(rng, (3, 1, 1, 64), "bf16"), make(rng, (3, 1, 1, 64), "bf16")
+
+    def odd(t, axes):
+        return t.as_strided(t.shape, [67 if i in axes else s for i, s in enumerate(t.stride())])
+
+    for kc, vc, n, axes in ((k, v, 50, (0, 2)), (k1, v1, 1, (1, 2))):
+        lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+        want, got = torch.empty_like(q), torch.full_like(q, 7)
+        with window.DecodePlan(max_seqs=1, d=64, page_size=kc.shape[1]) as plan:
+            plan.run(q, kc, vc, lens, want)
+            plan.run(odd(q, (0, 1)), odd(kc, axes), odd(vc, axes), lens, odd(got, (0, 1)))
+            plan.check()
+            assert torch.equal(got, want)
+            two = torch.zeros((2, 1, 64), dtype=torch.bfloat16, device="cuda")
+            with pytest.raises(syn.SynError):  # used: refused as before
+                plan.run(q, torch.zeros(67 * 64 + 64, dtype=torch.bfloat16, device="cuda").as_strided((2, *kc.shape[1:]), (67, 64, 64, 1)),
+                         two.view(2, 1, 1, 64).expand(2, *kc.shape[1:]), lens, want)
