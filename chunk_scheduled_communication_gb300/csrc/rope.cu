@@ -29,6 +29,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 #include <string>
 #include <vector>
@@ -678,6 +679,13 @@ int check_rows(const char *name, const void *p, int size, int heads, bool any) {
     return SYN_OK;
 }
 
+// Written rows may not overlap: heads, and tokens (or slots) where there are several
+int check_written(const char *name, int64_t token, int64_t head, int heads, int64_t rows, int d) {
+    if ((heads > 1 && std::abs(head) < d) || (heads > 0 && rows > 1 && std::abs(token) < d))
+        return host_fail(SYN_ERR_INVALID, std::string(name) + ": output rows overlap");
+    return SYN_OK;
+}
+
 enum Kind { kTurn, kNorm, kNormGrad };
 
 // Tokens whose rows of `heads` heads fill a block that walks `rows` rows, as
@@ -806,11 +814,13 @@ int run(syn_rope_plan_s *pl, Args &a, Kind kind, cudaStream_t st, int &grid) {
     return dispatch<float>(pl, a, kind, vec, st, grid);
 }
 
-int add(Args &a, const char *name, const syn_rope_rows_t *r, const void *w, int size, bool copy, bool scatter, bool norm) {
+int add(const syn_rope_cfg_t &c, Args &a, const char *name, const syn_rope_rows_t *r, const void *w, bool copy, bool scatter, bool norm) {
     if (r == nullptr) return SYN_OK;
+    const int size = elem_size(c.dtype);
     int rc;
     if ((rc = check_rows(name, r->x, size, r->heads, a.n_tokens > 0)) != SYN_OK || (rc = check_rows(name, r->y, size, r->heads, a.n_tokens > 0)) != SYN_OK ||
-        (rc = check_rows(name, w, size, 0, false)) != SYN_OK)
+        (rc = check_rows(name, w, size, 0, false)) != SYN_OK ||
+        (rc = check_written(name, r->y_token, r->y_head, r->heads, scatter ? a.n_slots : a.n_tokens, c.d)) != SYN_OK)
         return rc;
     if (r->heads == 0) return SYN_OK;
     Tensor &t = a.t[a.n_tensors++];
@@ -849,15 +859,13 @@ int forward(syn_rope_plan_s *pl, Kind kind, const syn_rope_rows_t *q, const void
     if (rc != SYN_OK) return rc;
     if (slots != nullptr && n_slots < 0) return host_fail(SYN_ERR_INVALID, "negative slot count");
     if (!(eps >= 0.f) || !std::isfinite(eps)) return host_fail(SYN_ERR_INVALID, "eps must be finite and not negative");
-    const int size = elem_size(pl->cfg.dtype);
     const bool norm = kind == kNorm, scatter = slots != nullptr;
-    if ((rc = add(a, "q", q, wq, size, false, false, norm)) != SYN_OK ||
-        (rc = add(a, "k", k, wk, size, false, scatter, norm)) != SYN_OK ||
-        (rc = add(a, "v", v, nullptr, size, true, scatter, false)) != SYN_OK)
-        return rc;
     a.slots = slots;
     a.n_slots = n_slots;
     a.eps = eps;
+    if ((rc = add(pl->cfg, a, "q", q, wq, false, false, norm)) != SYN_OK || (rc = add(pl->cfg, a, "k", k, wk, false, scatter, norm)) != SYN_OK ||
+        (rc = add(pl->cfg, a, "v", v, nullptr, true, scatter, false)) != SYN_OK)
+        return rc;
     int grid;
     return run(pl, a, kind, static_cast<cudaStream_t>(stream), grid);
 }
@@ -962,9 +970,8 @@ int syn_rope_backward(syn_rope_plan_t pl, const syn_rope_rows_t *dq, const syn_r
     Args a;
     int rc = begin(pl, a, positions, pos0, n_tokens);
     if (rc != SYN_OK) return rc;
-    const int size = elem_size(pl->cfg.dtype);
-    if ((rc = add(a, "dq", dq, nullptr, size, false, false, false)) != SYN_OK ||
-        (rc = add(a, "dk", dk, nullptr, size, false, false, false)) != SYN_OK)
+    if ((rc = add(pl->cfg, a, "dq", dq, nullptr, false, false, false)) != SYN_OK ||
+        (rc = add(pl->cfg, a, "dk", dk, nullptr, false, false, false)) != SYN_OK)
         return rc;
     a.sign = -1.f;
     int grid;
@@ -987,7 +994,8 @@ int syn_qk_norm_rope_backward(syn_rope_plan_t pl, const syn_rope_grad_t *q, cons
         if (g == nullptr) continue;
         if ((rc = check_rows(name, g->x, size, g->heads, n_tokens > 0)) != SYN_OK || (rc = check_rows(name, g->dy, size, g->heads, n_tokens > 0)) != SYN_OK ||
             (rc = check_rows(name, g->dx, size, g->heads, n_tokens > 0)) != SYN_OK || (rc = check_rows(name, g->w, size, 0, false)) != SYN_OK ||
-            (rc = check_rows(name, g->dw, 4, 0, false)) != SYN_OK)
+            (rc = check_rows(name, g->dw, 4, 0, false)) != SYN_OK ||
+            (rc = check_written(name, g->dx_token, g->dx_head, g->heads, n_tokens, pl->cfg.d)) != SYN_OK)
             return rc;
         if (g->heads == 0 || n_tokens == 0) {
             empty[x - 1] = g->dw;

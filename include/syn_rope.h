@@ -78,8 +78,9 @@ typedef struct {
 } syn_rope_cfg_t;
 
 /* Rows of one tensor: element (t, h, j) at x + t * x_token + h * x_head + j
- * (strides in elements, any sign of overlap but none between rows written).
- * y may be x with the same strides (in place). */
+ * (strides in elements, of any sign).  Rows that are read may overlap; written
+ * ones may not, and strides of y below d elements are refused where they are
+ * used.  y may be x with the same strides (in place). */
 typedef struct {
     const void *x;
     int64_t x_token, x_head;

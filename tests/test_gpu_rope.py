@@ -415,3 +415,32 @@ def test_a_new_plan_on_another_stream():
             plan.rotate(x, y, pos0=1000, stream=st)
             st.synchronize()
             assert torch.equal(y, ref)
+
+
+def test_overlapping_outputs_are_refused():
+    rng = np.random.default_rng(19)
+    x = make(rng, (4, 2, 64), "bf16")
+    w, dw = make(rng, (64,), "bf16"), torch.empty(64, device="cuda")
+    slots = torch.arange(4, device="cuda")
+    base = torch.full((4, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    bad = [base[:1].expand(4, 2, 64), base[:, :1].expand(4, 2, 64), base.view(-1).as_strided((4, 2, 64), (64, 32, 1))]
+    with rope.RopePlan(d=64) as plan:
+        for y in bad:
+            with pytest.raises(syn.SynError):
+                plan.rotate(x, y)
+            with pytest.raises(syn.SynError):
+                plan.norm_rotate(x, base, w, x, y, w, slots=slots)
+            with pytest.raises(syn.SynError):
+                plan.rotate_backward(x, y)
+            with pytest.raises(syn.SynError):
+                plan.norm_rotate_backward(x, x, y, w, dw)
+        torch.cuda.synchronize()
+        assert (base == 7).all()
+        # broadcast inputs are read as they are, and one row may have any stride
+        y, want = torch.empty_like(x), torch.empty_like(x)
+        plan.rotate(x[:1].expand(4, 2, 64), y)
+        plan.rotate(x[:1].expand(4, 2, 64).contiguous(), want)
+        assert torch.equal(y, want)
+        one = torch.empty_like(x[:1, :1])
+        plan.rotate(x[:1, :1], one.as_strided((1, 1, 64), (0, 0, 1)))
+        assert torch.equal(one, want[:1, :1])

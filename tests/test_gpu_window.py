@@ -607,3 +607,14 @@ def test_decode_strides_of_single_entries():
             with pytest.raises(syn.SynError):  # used: refused as before
                 plan.run(q, torch.zeros(67 * 64 + 64, dtype=torch.bfloat16, device="cuda").as_strided((2, *kc.shape[1:]), (67, 64, 64, 1)),
                          two.view(2, 1, 1, 64).expand(2, *kc.shape[1:]), lens, want)
+
+
+def test_decode_refuses_a_broadcast_output():
+    x = torch.zeros((4, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
+    q, lens = x[:, 0], torch.tensor([3] * 4, dtype=torch.int32, device="cuda")
+    with window.DecodePlan(max_seqs=4, H_q=2, H_kv=2, d=64, page_size=16) as plan:
+        for bad in (q[:1].expand(4, 2, 64), q[:, :1].expand(4, 2, 64)):
+            with pytest.raises(syn.SynError):
+                plan.run(q, x, x, lens, bad)
+        plan.run(q[:1].expand(4, 2, 64), x, x, lens, torch.empty_like(q))  # (a broadcast query is read as it is)
+        plan.check()
