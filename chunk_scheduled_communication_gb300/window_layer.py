@@ -67,7 +67,7 @@ class PagedCache:
     def __init__(self, layer, n_seqs, max_len, page=64):
         per = (max_len + page - 1) // page
         shape = (n_seqs * per, page, layer.H_kv, layer.d)
-        self.page = page
+        self.page, self.max_len, self.longest = page, per * page, 0
         self.k = torch.empty(shape, dtype=layer.type, device="cuda")
         self.v = torch.empty(shape, dtype=layer.type, device="cuda")
         self.table = torch.arange(n_seqs * per, dtype=torch.int32, device="cuda").view(n_seqs, per)
@@ -79,6 +79,13 @@ class PagedCache:
         """K and V as rows that `slots` index."""
         return self.k.flatten(0, 1), self.v.flatten(0, 1)
 
+    def grow(self, longest):
+        """The longest sequence is to have so many tokens (known to the host:
+        positions past the table would index out of it on the device)."""
+        if longest > self.max_len:
+            raise ValueError(f"a sequence of {longest} tokens in a cache of {self.max_len} a sequence")
+        self.longest = longest
+
     def slots(self, seq, pos):
         """Cache rows of positions `pos` of sequences `seq` (int64)."""
         return self.table[seq, pos // self.page].long() * self.page + pos % self.page
@@ -86,6 +93,9 @@ class PagedCache:
 
 def prompt(layer, plan, cache, qkv, lens):
     """The outputs of a packed batch of prompts; their K and V go to the cache."""
+    if len(lens) != cache.lens.shape[0]:
+        raise ValueError(f"{len(lens)} prompts for a cache of {cache.lens.shape[0]} sequences")
+    cache.grow(max(lens))
     n = torch.tensor(lens, device="cuda")
     seq = torch.repeat_interleave(torch.arange(len(lens), device="cuda"), n)
     pos = torch.cat([torch.arange(x, device="cuda") for x in lens])
@@ -104,6 +114,7 @@ def prompt(layer, plan, cache, qkv, lens):
 def decode(layer, cache, qkv):
     """One new token per sequence: its K (normed and rotated) and V are written
     into the cache in the pass that makes its query, then attended."""
+    cache.grow(cache.longest + 1)
     pos = cache.lens.long()
     q, k, v = layer.split(qkv)
     qr, out = torch.empty(q.shape, dtype=layer.type, device="cuda"), torch.empty(q.shape, dtype=layer.type, device="cuda")

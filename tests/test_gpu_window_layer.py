@@ -66,3 +66,21 @@ def test_training_step_and_decoding():
     assert off(r["dwq"], wq.grad) <= 8 * U and off(r["dwk"], wk.grad) <= 8 * U
     # two ways to the same rows: each within (2 u + 2^-14) of max|v|
     assert r["worst"] <= 2 * (2 * U + 2.0 ** -14) * r["v_max"]
+
+
+def test_a_cache_that_is_full():
+    """Refused on the host, before any position indexes past the page table."""
+    layer = window_layer.WindowLayer(2, 1, 64, 16, 2)
+    cache = window_layer.PagedCache(layer, 2, 20, page=8)  # 24 tokens a sequence
+    rows = lambda n: torch.randn(n, 4, 64, device="cuda").bfloat16()
+    for bad in ([25, 3], [3], [1, 2, 3]):
+        with pytest.raises(ValueError):
+            window_layer.prompt(layer, layer.plan(bad), cache, rows(sum(bad)), bad)
+    window_layer.prompt(layer, layer.plan([22, 3]), cache, rows(25), [22, 3])
+    for _ in range(2):
+        window_layer.decode(layer, cache, rows(2))
+    before = cache.k.clone()
+    with pytest.raises(ValueError):
+        window_layer.decode(layer, cache, rows(2))
+    cache.plan.check()
+    assert cache.lens.tolist() == [24, 5] and torch.equal(cache.k.nan_to_num(), before.nan_to_num())
