@@ -203,9 +203,12 @@ def _ptr(t) -> int:
 
 
 def _stream(stream) -> int:
-    if stream is None:  # the current device's current stream, without building a Stream object
+    if stream is None:
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        try:  # without building a Stream object (3 us of a small call), where torch has these functions
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:
+            return int(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
