@@ -423,7 +423,7 @@ bool al16(const void *x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }
 
 // (a stride of an axis with one entry is never used)
 int check_cache(const char *name, const syn_window_cache_t *c, int64_t pages, int page_size, int heads) {
-    if (c == nullptr || c->p == nullptr) return host_fail(SYN_ERR_INVALID, std::string(name) + ": null operand");
+    if (c == nullptr || (pages > 0 && c->p == nullptr)) return host_fail(SYN_ERR_INVALID, std::string(name) + ": null operand");
     if (!al16(c->p)) return host_fail(SYN_ERR_INVALID, std::string(name) + ": operand not 16-byte aligned");
     if ((pages > 1 && c->page % 8 != 0) || (page_size > 1 && c->token % 8 != 0) || (heads > 1 && c->head % 8 != 0))
         return host_fail(SYN_ERR_INVALID, std::string(name) + ": strides must be multiples of 8 elements");

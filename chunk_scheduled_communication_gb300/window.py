@@ -227,7 +227,8 @@ class DecodePlan:
             if page_table.dtype is not _int32 or not page_table.is_cuda or len(shape) != 2 or shape[0] != n or \
                     not page_table.is_contiguous():
                 raise ValueError(f"page_table must be a contiguous CUDA tensor [{n}, pages] of int32")
-            table, stride = page_table.data_ptr(), shape[1]
+            # (a table without entries has no address, and no table would mean a contiguous cache: any address, never read)
+            table, stride = page_table.data_ptr() or lens, shape[1]
         _check(self._decode(self._h, qr, k, v, table, stride, pages, lens, n, out, _lse(lse, n, heads),
                                          syn._stream(stream)), "syn_window_decode")
 

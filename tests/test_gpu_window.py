@@ -618,3 +618,18 @@ def test_decode_refuses_a_broadcast_output():
                 plan.run(q, x, x, lens, bad)
         plan.run(q[:1].expand(4, 2, 64), x, x, lens, torch.empty_like(q))  # (a broadcast query is read as it is)
         plan.check()
+
+
+def test_decode_with_an_empty_table_or_cache():
+    """A table without pages names no key; it is not a missing table."""
+    rng = np.random.default_rng(20)
+    k, v, q = make(rng, (3, 16, 1, 64), "bf16"), make(rng, (3, 16, 1, 64), "bf16"), make(rng, (2, 1, 64), "bf16")
+    out, lse = torch.full_like(q, 7), torch.full((2, 1), 7.0, device="cuda")
+    table = torch.empty((2, 0), dtype=torch.int32, device="cuda")
+    with window.DecodePlan(max_seqs=2, d=64, page_size=16) as plan:
+        for kc, vc in ((k, v), (k[:0], v[:0]), (torch.empty_like(k[:0]), torch.empty_like(v[:0]))):
+            for n, status in (([5, 0], syn.ERR_BOUNDS), ([0, 0], syn.OK)):
+                out.fill_(7), lse.fill_(7)
+                plan.run(q, kc, vc, torch.tensor(n, dtype=torch.int32, device="cuda"), out, lse=lse, page_table=table)
+                assert plan.sync() == status
+                assert not out.any() and torch.isneginf(lse).all()
