@@ -516,7 +516,7 @@ int syn_window_decode(syn_decode_plan_t pl, const syn_window_rows_t *q, const sy
         (rc = check_cache("k", k, n_pages, c.page_size, c.H_kv)) != SYN_OK ||
         (rc = check_cache("v", v, n_pages, c.page_size, c.H_kv)) != SYN_OK)
         return rc;
-    if ((n_seqs > 1 && O->token <= 0) || (c.H_q > 1 && O->head <= 0)) return host_fail(SYN_ERR_INVALID, "O: strides must be positive");
+    if ((n_seqs > 1 && O->token < c.d) || (c.H_q > 1 && O->head < c.d)) return host_fail(SYN_ERR_INVALID, "O: output rows overlap");
     if (seq_lens == nullptr) return host_fail(SYN_ERR_INVALID, "null seq_lens");
     if (n_pages < 0 || n_pages >= (int64_t)1 << 31) return host_fail(SYN_ERR_INVALID, "n_pages must be in [0, 2^31)");
     if (page_table != nullptr && table_stride < 0) return host_fail(SYN_ERR_INVALID, "negative table_stride");

@@ -334,6 +334,12 @@ int check_rows(const char *name, const syn_window_rows_t *r, int64_t rows, int h
     return SYN_OK;
 }
 
+// Written rows may not overlap
+int check_written(const char *name, const syn_window_rows_t *r, int64_t rows, int heads, int d) {
+    if ((rows > 1 && r->token < d) || (heads > 1 && r->head < d)) return host_fail(SYN_ERR_INVALID, std::string(name) + ": output rows overlap");
+    return SYN_OK;
+}
+
 int encode(CUtensorMap *m, const syn_window_plan_s *pl, const syn_window_rows_t &r, int64_t rows, int heads, uint32_t box_rows) {
     // a stride of an axis with one entry is never used; keep it valid
     const int64_t d = pl->cfg.d, head = heads > 1 ? r.head : d, token = rows > 1 ? r.token : d * heads;
@@ -516,7 +522,8 @@ int syn_window_attention(syn_window_plan_t pl, const syn_window_rows_t *Q, const
     const int64_t nq = pl->info.q_rows, nk = pl->info.k_rows;
     int rc;
     if ((rc = check_rows("Q", Q, nq, c.H_q)) != SYN_OK || (rc = check_rows("K", K, nk, c.H_kv)) != SYN_OK ||
-        (rc = check_rows("V", V, nk, c.H_kv)) != SYN_OK || (rc = check_rows("O", O, nq, c.H_q)) != SYN_OK)
+        (rc = check_rows("V", V, nk, c.H_kv)) != SYN_OK || (rc = check_rows("O", O, nq, c.H_q)) != SYN_OK ||
+        (rc = check_written("O", O, nq, c.H_q, c.d)) != SYN_OK)
         return rc;
     if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return host_fail(SYN_ERR_INVALID, "lse: not aligned");
     if (nq == 0) return SYN_OK;
@@ -555,7 +562,9 @@ int syn_window_attention_backward(syn_window_plan_t pl, const syn_window_rows_t 
     if ((rc = check_rows("dO", dO, nq, c.H_q)) != SYN_OK || (rc = check_rows("Q", Q, nq, c.H_q)) != SYN_OK ||
         (rc = check_rows("K", K, nk, c.H_kv)) != SYN_OK || (rc = check_rows("V", V, nk, c.H_kv)) != SYN_OK ||
         (rc = check_rows("O", O, nq, c.H_q)) != SYN_OK || (rc = check_rows("dQ", dQ, nq, c.H_q)) != SYN_OK ||
-        (rc = check_rows("dK", dK, nk, c.H_kv)) != SYN_OK || (rc = check_rows("dV", dV, nk, c.H_kv)) != SYN_OK)
+        (rc = check_rows("dK", dK, nk, c.H_kv)) != SYN_OK || (rc = check_rows("dV", dV, nk, c.H_kv)) != SYN_OK ||
+        (rc = check_written("dQ", dQ, nq, c.H_q, c.d)) != SYN_OK || (rc = check_written("dK", dK, nk, c.H_kv, c.d)) != SYN_OK ||
+        (rc = check_written("dV", dV, nk, c.H_kv, c.d)) != SYN_OK)
         return rc;
     if (nq > 0 && (lse == nullptr || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0))
         return host_fail(SYN_ERR_INVALID, "lse: null or not aligned");

@@ -55,7 +55,7 @@ typedef struct {
 
 /* A tensor [rows, heads, d]: element (t, h, j) at p + t * token + h * head + j.
  * p 16-byte aligned, strides positive multiples of 8 elements (where the
- * tensor has more than one row or head). */
+ * tensor has more than one row or head), those of outputs d or more. */
 typedef struct {
     void *p;
     int64_t token, head;

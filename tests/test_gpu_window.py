@@ -633,3 +633,39 @@ def test_decode_with_an_empty_table_or_cache():
                 plan.run(q, kc, vc, torch.tensor(n, dtype=torch.int32, device="cuda"), out, lse=lse, page_table=table)
                 assert plan.sync() == status
                 assert not out.any() and torch.isneginf(lse).all()
+
+
+def test_overlapping_outputs_are_refused():
+    x = torch.zeros((6, 2, 64), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((6, 2), device="cuda")
+    bad = [x.view(-1).as_strided((6, 2, 64), s) for s in ((8, 64, 1), (128, 8, 1), (32, 384, 1))]
+    c = torch.zeros((6, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
+    lens = torch.tensor([3] * 6, dtype=torch.int32, device="cuda")
+    with window.WindowPlan([6], H_q=2, H_kv=2, d=64, backward=True) as plan, \
+            window.DecodePlan(max_seqs=6, H_q=2, H_kv=2, d=64, page_size=16) as step:
+        for y in bad:
+            with pytest.raises(syn.SynError):
+                plan.forward(x, x, x, y)
+            for i in range(3):
+                g = [torch.zeros_like(x) for _ in range(3)]
+                g[i] = y
+                with pytest.raises(syn.SynError):
+                    plan.backward(x, x, x, x, x, lse, *g)
+            with pytest.raises(syn.SynError):
+                step.run(x, c, c, lens, y)
+
+
+def test_a_sequence_of_thousands_of_rows():
+    """Many blocks a row, sums in parts, a window and sinks far apart."""
+    case = ([2503], [2700], 2, 1, 128, 900, 20)
+    q, k, v, do = setup(case, "bf16")
+    _, u, tiny = TYPES["bf16"]
+    r, lse_ref = reference(f64(q), f64(k), f64(v), case[0], case[1], case[5], case[6], u, tiny, f64(do))
+    with plan_of(case, "bf16") as plan:
+        assert plan.info()["n_parts"] > 0
+        out, lse, dq, dk, dv = run(plan, q, k, v, do)
+    near(out, r["O"], r["eO"])
+    near_lse(lse, lse_ref)
+    near(dq, r["dQ"], r["eQ"])
+    near(dk, r["dK"], r["eK"])
+    near(dv, r["dV"], r["eV"])
