@@ -1,8 +1,9 @@
 // decode.cu -- windowed attention of one query token per sequence over a paged
 // cache, and its C ABI (include/syn_window.h).
 //
-// Every visible key and value row is read once and meets the group's query
-// heads only, so HBM bounds a full batch and latency a small one.  A CTA takes
+// Every visible key and value row meets its group's query heads only and is read
+// once for each 16 of them, so HBM bounds a full batch and latency a small one
+// (groups above 16 heads read their rows several times).  A CTA takes
 // one sequence, one kv head, up to 16 of its query heads and one of `splits`
 // ranges of the visible keys (the sinks and the window as one index space), 64
 // keys a tile.  Each of 128 threads resolves the page of one K or V row of a
@@ -15,10 +16,10 @@
 // ranges' order.
 //
 // Measured on one GB300 (bf16, 32/8 heads of 128): 128 sequences at window 4096,
-// 2.15 GB of visible rows, 346 to 348 us, 6.2 TB/s, 0.91 of the measured copy rate
+// 2.15 GB of visible rows, 348 us, 6.2 TB/s, 0.91 of the measured copy rate
 // (two stages and three CTAs an SM; three and two 419 us, six and one 802 us; the
 // rows of the join that no query head has written too 358 us); three sequences
-// at window 1024 10.3 us, a chain of dependent loads (length, page, row; the
+// at window 1024 9.8 to 10.2 us, a chain of dependent loads (length, page, row; the
 // query and the second tile's page beside it: 1 us less) and the join through
 // memory (one through the shared memory of a cluster's CTAs: no change).
 #include <cuda_bf16.h>
@@ -46,7 +47,7 @@ constexpr int kDecCtas = 3;        // resident on an SM
 constexpr int kMaxSplits = 128;
 constexpr int kWaves = 6;          // CTAs wanted per resident slot
 constexpr uint64_t kDrainNs = 1000000000;  // more for copies under way, after a wait past the limit
-constexpr int kMinTiles = 1;       // tiles of a range at least, where there are that many
+constexpr int kMinTiles = 1;       // whole tiles wanted for a range
 
 struct DecParams {
     const void *q, *k, *v;
@@ -561,8 +562,10 @@ int syn_window_decode(syn_decode_plan_t pl, const syn_window_rows_t *q, const sy
     p.page_shift = -1;
     for (int b = 0; b < 31; ++b)
         if (c.page_size == 1 << b) p.page_shift = b;
-    // Ranges: enough CTAs for kWaves rounds of the resident ones, but ranges of
-    // no less than kMinTiles tiles of the longest sequence the table allows.
+    // Ranges: enough CTAs for kWaves rounds of the resident ones, but no more of
+    // them than whole tiles that the longest sequence the table allows has.  The
+    // count is rounded down and a range's tiles up, so 17 tiles (window 1024 and a
+    // few sinks) make 16 ranges of two, of which nine have any.
     const int64_t n = (int64_t)n_seqs * c.H_kv * pl->hgroups;
     const int64_t longest = std::min<int64_t>(p.cap, c.window + (int64_t)c.sinks);
     const int64_t most = std::min<int64_t>(kMaxSplits, std::max<int64_t>(1, longest / (kTileKeys * kMinTiles)));

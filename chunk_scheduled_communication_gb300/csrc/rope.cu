@@ -14,15 +14,17 @@
 // these are under way, and then walk the rows.
 //
 // Measured on one GB300 (bf16, heads of 128; back-to-back calls): the rotation of
-// 32768 tokens x 40 heads 98.5 us, 6.8 TB/s, the measured copy rate;
+// 32768 tokens x 40 heads 98.2 us, 6.8 TB/s, the measured copy rate;
 // with the norm, 16384 tokens 57.6 us, 5.8 TB/s (0.86: 310 instructions for a
-// warp's four rows fill two thirds of the issue slots); its gradient 91.8 us,
-// 5.5 TB/s (0.81: 127 registers, 16 warps an SM).  A call on a few tokens takes
-// 2.7-3.3 us on the device and 7-8.3 us with its host side.
+// warp's four rows fill two thirds of the issue slots); its gradient 91.3 us,
+// 5.5 TB/s (0.81: 125 registers, 16 warps an SM).  A call on a few tokens takes
+// 2.4-3.0 us in a graph and 6.6-8.4 us with its host side.
 //
 // The angle of position p and frequency f is p * f mod 2 pi.  f / 2 pi is kept
 // as a 64-bit fraction of a turn; the 64-bit product with p drops whole turns
-// exactly, and the upper 32 bits give the angle in half turns to sincospif.
+// exactly, and the upper 32 bits give the angle in half turns to sincospif.  What
+// remains is the rounding of f / 2 pi to 53 bits, about 3e-16 p f radians, and
+// that of the angle to fp32, about 1e-7.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

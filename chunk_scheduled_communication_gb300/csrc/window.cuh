@@ -345,9 +345,11 @@ cudaError_t bwd_sum_launch(bool bf16, int n_items, const SumParams &p, cudaStrea
 
 // Launch a kernel whose blocks may start, as far as ptx::grid_wait, while the
 // stream's kernel before it ends: its launch, its barriers, TMEM and work list
-// cost no time of their own (back-to-back calls on one GB300: a rotation of 8
-// tokens 4.3 -> 2.75 us, a decode of 3 sequences 12.4 -> 10.3, the five launches
-// of a ragged training step 117.7 -> 104.7).  No kernel lets the next one start
+// cost less (calls in a graph on one GB300, without and with it: a rotation of 8
+// tokens 2.7, 2.4 us; norm and rotation of 4 3.5, 3.0; a decode of 3 sequences
+// 10.5, 10.1; the five launches of a ragged training step 97.8, 96.1).  The kernel
+// before may be of another kind that lets its successor start at its own
+// beginning, so every thread of these waits.  None of these lets the next one start
 // before its own blocks end: that took the SMs' places out of the order the
 // work is dealt in (gradient at 16384 tokens 1980 -> 2015 us, decode 10.3 -> 11.2).
 template <typename... P, typename... A>

@@ -29,7 +29,7 @@
 // are under way at a time.
 //
 // Measured on one GB300 (bf16, 16384 tokens, 32/8 heads of 128, window 2048, 4
-// sinks): 855 us, tensor pipe 55 % active.  It is bound by the round trip of dP's
+// sinks): 866 us, tensor pipe 59 % active.  It is bound by the round trip of dP's
 // one place -- product, commit, load, arrival -- beside products of 64 columns,
 // which cost the pipe 48 to 58 cycles where 32 would be the peak's pace.  Blocks
 // of 128 queries, S and dP with P and dS over them, had less to overlap (1115

@@ -25,8 +25,9 @@
 // hand, so it takes rowsum(P dP) instead and leaves it for dK and dV, whose
 // kernel runs after this one.
 //
-// Measured as window_dkv.cu: 560 us, tensor pipe 62 % active (blocks of 64 keys
-// in one ring, as there: 881 us; both tiles in one ring of two: 840 us).
+// Measured as window_dkv.cu: 625 us, tensor pipe 57 % active (560 us, 62 %, before
+// the tiles of one block took their own rowsum; then blocks of 64 keys in one
+// ring, as there: 881 us; both tiles in one ring of two: 840 us).
 #include "window.cuh"
 
 namespace syn {

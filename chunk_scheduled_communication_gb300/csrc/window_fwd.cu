@@ -31,8 +31,9 @@
 // accumulator is rescaled only when a block raises it by more.
 //
 // Measured on one GB300 (bf16, 16384 tokens, 32 query and 8 kv heads of 128, 4
-// sinks): window 4096 705 us, 1366 TFLOP/s over the visible pairs, 0.70 of the
-// measured burst peak; window 2048 440 us.  Tensor pipe 58 % active: a product of
+// sinks): window 4096 711 us alone, 1354 TFLOP/s over the visible pairs, 0.70 of
+// the measured burst peak, and 743 to 750 in long runs, under the power cap; window
+// 2048 444 us.  Tensor pipe 60 % active: a product of
 // 80 columns costs it 52 cycles where 40 would be the peak's pace (128 columns:
 // 64), but blocks of 128 keys would leave the probabilities no columns but the
 // scores', and each step would wait for the last one's P.V.  A step takes the

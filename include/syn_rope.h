@@ -30,9 +30,10 @@
  *
  * Precision: inputs in the plan's type, arithmetic in fp32, one
  * round-to-nearest-even to the plan's type.  position * f_i is reduced modulo
- * one turn exactly (64-bit fixed point), so the angle of any int64 position
- * whose product with the table's 2^-64-turn steps matters is right to about 1e-7
- * radians; negative positions are allowed.  The norm's sums are fp32.
+ * one turn exactly (64-bit fixed point); an angle is right to about 1e-7 radians
+ * (its rounding to fp32) and 3e-16 |position| f_i (that of f_i to 53 bits): to
+ * 2e-7 at positions below 2^28, 1e-6 below 2^31.  Negative positions are allowed.
+ * The norm's sums are fp32.
  */
 #ifndef SYN_ROPE_H
 #define SYN_ROPE_H

@@ -23,8 +23,9 @@
  * in the gradient the score gradients) are rounded to the inputs' type as
  * operands of the next product; outputs are rounded once.  A value row V[j]
  * that is not finite reaches the rows of every 128-row query tile that reads
- * its block, as 0 * inf does in a matrix product, and a query or dO row that is
- * not finite the gradients of the keys in the tiles that its block meets; rows
+ * its block, as 0 * inf does in a matrix product, a key or value row that is not
+ * finite likewise the dQ of such tiles' rows, and a query or dO row that is not
+ * finite the gradients of the keys in the tiles that its block meets; rows
  * outside a sequence (another sequence's, an unused part of a page) never do.
  */
 #ifndef SYN_WINDOW_H
@@ -75,7 +76,11 @@ int syn_window_cfg_default(syn_window_cfg_t *cfg);
 /* Validate the lengths and build the plan's work lists on the current device.
  * The lists give each SM about the same number of key blocks; they depend on
  * the lengths alone, so a plan serves any number of calls (layers, steps)
- * with these lengths. */
+ * with these lengths.  Making one allocates and copies with blocking calls and
+ * waits for the device, all streams of it: 0.14 ms for a token, 0.3 for 16384 rows
+ * of one sequence, 0.7 for 128 sequences; with backward 0.2, 0.9 and 2.3 (32/8
+ * heads).  Lists of 2^28 tiles or more, or that host memory cannot hold, are
+ * SYN_ERR_UNSUPPORTED. */
 int syn_window_plan_create(syn_window_plan_t *out, const syn_window_cfg_t *cfg, int n_seqs, const int64_t *q_lens,
                            const int64_t *k_lens);
 
