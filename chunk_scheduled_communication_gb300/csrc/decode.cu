@@ -46,7 +46,6 @@ constexpr int kDecStages = 2;
 constexpr int kDecCtas = 3;        // resident on an SM
 constexpr int kMaxSplits = 128;
 constexpr int kWaves = 6;          // CTAs wanted per resident slot
-constexpr uint64_t kDrainNs = 1000000000;  // more for copies under way, after a wait past the limit
 constexpr int kMinTiles = 1;       // whole tiles wanted for a range
 
 struct DecParams {

@@ -91,14 +91,19 @@ __device__ __forceinline__ bool poll_bar(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
+constexpr uint64_t kDrainNs = 1000000000;  // limit of the waits on the way out, at least
+
 // The rest of a wait: bounded.  A wait that runs out records SYN_ERR_TIMEOUT and
 // sets `abort`, after which no wait lasts; the warp goes on, with wrong results
-// but within its buffers, to the end of its loop.
+// but within its buffers, to the end of its loop.  The producer stops (a barrier
+// whose copies are still under way is not armed again) and waits for what it has
+// issued, as the issuers do; these waits have a limit of their own, so that a short
+// one of the caller's does not end a CTA before its copies and products.
 __device__ __forceinline__ void wait_long(uint32_t bar, uint32_t parity, volatile int *abort, const Common &p) {
-    const uint64_t t0 = ptx::globaltimer();
+    const uint64_t t0 = ptx::globaltimer(), limit = abort != nullptr || p.timeout_ns > kDrainNs ? p.timeout_ns : kDrainNs;
     while (!poll_bar(bar, parity)) {
         if (abort != nullptr && *abort != 0) return;
-        const bool late = ptx::globaltimer() - t0 > p.timeout_ns;
+        const bool late = ptx::globaltimer() - t0 > limit;
         if (late && atomicCAS(p.err, 0, SYN_ERR_TIMEOUT) == 0) {
             p.err[1] = WHERE_PIPE;
             p.err[2] = (int)blockIdx.x;
@@ -120,6 +125,10 @@ __device__ __forceinline__ void wait_bar(uint32_t bar, uint32_t parity, volatile
     if (!poll_bar(bar, parity)) wait_long(bar, parity, abort, p);
     __syncwarp();
 }
+
+// Whether a wait of the CTA ran out (one read of a converged warp: the same for
+// all its lanes)
+__device__ __forceinline__ bool aborted(volatile int *abort) { return *abort != 0; }
 
 // Wait used while draining on the way out: ignores the abort flag.
 __device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity, const Common &p) {

@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
             for (; wk.next(p, b); ++g) {
                 if (b.first) {
                     wait_bar(bar(B_XE), (ic & 1u) ^ 1u, abort, c);
+                    if (aborted(abort)) break;
                     if (lane == 0) {
                         ptx::mbar_arrive_expect_tx(bar(B_XF), 2 * L::kTileX);
                         for (int x = 0; x < D / 64; ++x) {
@@ -178,6 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
                 }
                 const int s = (int)(g % kStages);
                 wait_bar(bar(B_UE + s), ((g / kStages) & 1u) ^ 1u, abort, c);
+                if (aborted(abort)) break;
                 if (lane == 0) {
                     const uint32_t u = sbase + (uint32_t)(L::RING + s * L::kStage);
                     const int row = wk.it->stream0 + b.start;

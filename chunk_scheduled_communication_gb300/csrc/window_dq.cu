@@ -156,10 +156,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_con
         Ring<kWStages> w;
         if (warp == 0) {
             // ================= TMA producer =================
-            for (int i = i0; i < i1; ++i) {
+            bool stop = false;
+            uint32_t n_x = 0, n_w = 0;  // items whose X and Y, blocks whose W has been issued (g: U)
+            for (int i = i0; i < i1 && !stop; ++i) {
                 const BwdItem &it = p.items[i];
                 const int n_sink = sink_blocks(it), n = blocks_of(it), hk = it.hk, row0 = it.stream0, q_row = it.row0, h = it.h0;
                 wait_bar(bar(B_XE), ((uint32_t)(i - i0) & 1u) ^ 1u, abort, c);
+                if (aborted(abort)) break;
+                ++n_x;
                 if (lane == 0) {
                     ptx::mbar_arrive_expect_tx(bar(B_XF), 2 * L::kTile);
                     for (int x = 0; x < D / 64; ++x) {
@@ -168,9 +172,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_con
                     }
                 }
                 __syncwarp();
-                for (int k = 0; k < n; ++k, ++g, u.next(), w.next()) {
+                for (int k = 0; k < n; ++k, u.next(), w.next()) {
                     step(b, k, n_sink, it);
                     wait_bar(bar(B_UE + u.s), u.phase ^ 1u, abort, c);
+                    stop = aborted(abort);
+                    if (stop) break;
+                    ++g;
                     if (lane == 0) {
                         ptx::mbar_arrive_expect_tx(bar(B_UF + u.s), L::kTile);
                         for (int x = 0; x < D / 64; ++x)
@@ -179,6 +186,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_con
                     }
                     __syncwarp();
                     wait_bar(bar(B_WE + w.s), w.phase ^ 1u, abort, c);
+                    stop = aborted(abort);
+                    if (stop) break;
+                    ++n_w;
                     if (lane == 0) {
                         ptx::mbar_arrive_expect_tx(bar(B_WF + w.s), L::kTile);
                         for (int x = 0; x < D / 64; ++x)
@@ -189,11 +199,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_con
                 }
             }
             // every load issued must land before the CTA exits
-            if (i1 > i0) drain_bar(bar(B_XF), (uint32_t)(i1 - i0 - 1) & 1u, c);
+            if (n_x > 0) drain_bar(bar(B_XF), (n_x - 1u) & 1u, c);
             for (uint32_t s = 0; s < kUStages; ++s)
                 if (g > s) drain_bar(bar(B_UF + (int)s), ((g - 1u - s) / kUStages) & 1u, c);
             for (uint32_t s = 0; s < kWStages; ++s)
-                if (g > s) drain_bar(bar(B_WF + (int)s), ((g - 1u - s) / kWStages) & 1u, c);
+                if (n_w > s) drain_bar(bar(B_WF + (int)s), ((n_w - 1u - s) / kWStages) & 1u, c);
         } else if (warp == 1) {
             // ================= S = X U^T =================
             const uint32_t x_d = desc_lo(sbase + L::X, 16), u_d = desc_lo(sbase + L::U, 16);

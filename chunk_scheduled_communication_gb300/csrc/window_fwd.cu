@@ -203,10 +203,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
         uint32_t g = 0;
         if (warp == 0) {
             // ================= TMA producer =================
-            for (int i = 0; i < n_items; ++i) {
+            bool stop = false;
+            int n_q = 0;  // items whose Q has been issued
+            for (int i = 0; i < n_items && !stop; ++i) {
                 const FwdItem &it = item_at(i);
                 const int n_blk = it.n_blk, n_sink = (it.s_end + kBK - 1) / kBK, hk = it.hk, row0 = it.kv_row0;
                 wait_bar(bar(B_QE), ((uint32_t)i & 1u) ^ 1u, abort, c);
+                if (aborted(abort)) break;
+                ++n_q;
                 if (lane == 0) {
                     ptx::mbar_arrive_expect_tx(bar(B_QF), kTiles * L::kTileQ);
                     for (int t = 0; t < kTiles; ++t)
@@ -218,6 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                 for (int k = 0; k < n_blk; ++k, ++g, r.next<kStages>()) {
                     step<kBK>(b, k, n_sink, it);
                     wait_bar(bar(B_KE + r.s), r.phase ^ 1u, abort, c);
+                    stop = aborted(abort);
+                    if (stop) break;
                     if (lane == 0) {
                         const uint32_t br = bar(B_KF + r.s), dk = sK + (uint32_t)(r.s * L::kTileK), dv = sV + (uint32_t)(r.s * L::kTileK);
                         ptx::mbar_arrive_expect_tx(br, (uint32_t)(2 * b.nk * D * 2));
@@ -238,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
                 }
             }
             // every load issued must land before the CTA exits
-            if (n_items > 0) drain_bar(bar(B_QF), (uint32_t)(n_items - 1) & 1u, c);
+            if (n_q > 0) drain_bar(bar(B_QF), (uint32_t)(n_q - 1) & 1u, c);
             for (uint32_t s = 0; s < kStages; ++s)
                 if (g > s) drain_bar(bar(B_KF + (int)s), ((g - 1u - s) / kStages) & 1u, c);
         } else if (warp <= 2) {

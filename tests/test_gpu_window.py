@@ -669,3 +669,19 @@ def test_a_sequence_of_thousands_of_rows():
     near(dq, r["dQ"], r["eQ"])
     near(dk, r["dK"], r["eK"])
     near(dv, r["dV"], r["eV"])
+
+
+def test_waits_that_run_out():
+    """A limit that no wait is sure to meet: the calls end, and the next plan's are right."""
+    case = ([1500, 3], [1500, 3], 4, 2, 128, 0, 0)
+    q, k, v, do = setup(case, "bf16")
+    with plan_of(case, "bf16") as plan, plan_of(case, "bf16", timeout_ns=1) as short:
+        want = run(plan, q, k, v, do)
+        got = [torch.empty_like(t) for t in want]
+        for _ in range(3):
+            short.forward(q, k, v, got[0], lse=got[1])
+            status = short.sync()
+            assert status in (syn.OK, syn.ERR_TIMEOUT)
+            short.backward(do, q, k, v, want[0], want[1], *got[2:])
+            assert short.sync() in (syn.OK, syn.ERR_TIMEOUT)
+            assert all(torch.equal(a, b) for a, b in zip(run(plan, q, k, v, do), want))

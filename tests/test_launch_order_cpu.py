@@ -107,3 +107,25 @@ def test_decode_waits_leave_a_warp_whole_and_a_lost_copy_ends_the_loading():
     # a barrier whose rows never came is not armed again
     assert "&& !lost) load(t +" in text and "if (!lost) lost = !landed(" in text
     assert "SYN_ERR_TIMEOUT ?" in text
+
+
+def test_producers_stop_after_a_wait_that_ran_out():
+    """A barrier whose copies are still under way is not armed again: between a
+    producer's wait for a free stage and its next copies it asks whether a wait ran
+    out, and the waits on the way out have a limit of their own."""
+    found = 0
+    for text in sources():
+        at = text.find("if (warp == 0) {")
+        if "tma_load_3d" not in text or "__global__" not in text:
+            continue
+        producer = text[at:closing(text, text.index("{", at), "{}")]
+        waits = [m.start() for m in re.finditer(r"(?<!\w)wait_bar\(", producer)]
+        armed = [m.start() for m in re.finditer("mbar_arrive_expect_tx", producer)]
+        assert len(waits) == len(armed) > 0
+        for w, a in zip(waits, armed):
+            assert w < producer.index("aborted(abort)", w) < a
+        found += 1
+    assert found == 3
+    shared = next(t for t in sources() if "void drain_bar" in t and "launch_early" in t)
+    wait = shared[shared.index("void wait_long"):shared.index("void wait_bar")]
+    assert "kDrainNs" in wait
