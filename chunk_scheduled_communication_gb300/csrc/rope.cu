@@ -18,7 +18,7 @@
 // with the norm, 16384 tokens 57.6 us, 5.8 TB/s (0.86: 310 instructions for a
 // warp's four rows fill two thirds of the issue slots); its gradient 91.3 us,
 // 5.5 TB/s (0.81: 125 registers, 16 warps an SM).  A call on a few tokens takes
-// 2.4-3.0 us in a graph and 6.6-8.4 us with its host side.
+// 2.4-3.0 us in a graph and 6.6-9.0 us with its host side.
 //
 // The angle of position p and frequency f is p * f mod 2 pi.  f / 2 pi is kept
 // as a 64-bit fraction of a turn; the 64-bit product with p drops whole turns

@@ -31,8 +31,8 @@
 // accumulator is rescaled only when a block raises it by more.
 //
 // Measured on one GB300 (bf16, 16384 tokens, 32 query and 8 kv heads of 128, 4
-// sinks): window 4096 711 us alone, 1354 TFLOP/s over the visible pairs, 0.70 of
-// the measured burst peak, and 743 to 750 in long runs, under the power cap; window
+// sinks): window 4096 710 us alone, 1356 TFLOP/s over the visible pairs, 0.70 of
+// the measured burst peak, and 735 to 754 in long runs, under the power cap; window
 // 2048 444 us.  Tensor pipe 60 % active: a product of
 // 80 columns costs it 52 cycles where 40 would be the peak's pace (128 columns:
 // 64), but blocks of 128 keys would leave the probabilities no columns but the
