@@ -24,7 +24,6 @@ EPS = 1e-5
 CLIP_EPS = 1e-6
 MOST_FLOPS = 12 * 4096 * 4096 * 14336      # of a gated block's case
 MOST_CLIP = 218 << 20                      # elements of a clipping case
-LONG_LIST = 60                             # tensors that are clipped into one tensor for each type, not a list
 
 
 # ---------------------------------------------------------------------------------------- cases
@@ -91,19 +90,6 @@ def _tensors(case):
     return [(int(s * scale), rng.choice(kinds)) for s in share]
 
 
-def _joined(case, values):
-    """The values of a clipping case's tensors: a list, and of a long one a tensor for each type, in which
-    every tensor begins at a multiple of 8 elements."""
-    if len(values) < LONG_LIST:
-        return values
-    kinds, out = [k for _, k in _tensors(case)], []
-    for kind in sorted(set(kinds)):
-        mine = [t for t, k in zip(values, kinds) if k == kind]
-        gap = mine[0].new_zeros(7)
-        out.append(torch.cat([p for t in mine for p in (t, gap[:-t.numel() % 8])]))
-    return out
-
-
 def work(case):
     c = case
     if c["op"] == "clip":
@@ -160,14 +146,6 @@ def prepare(case, seed):
     new = lambda *shape, dtype: torch.empty(*shape, dtype=dtype, device="cuda")
     if c["op"] == "clip":
         s["out"] = [torch.empty_like(t) for t in x["grads"]]
-        s["result"] = _joined(c, s["out"])
-        if s["result"] is not s["out"]:  # the outputs are views of what is returned
-            kinds, sizes = [k for _, k in _tensors(c)], [t.numel() for t in s["out"]]
-            for kind, flat in zip(sorted(set(kinds)), s["result"]):
-                mine, at = [i for i, k in enumerate(kinds) if k == kind], 0
-                for i in mine:
-                    s["out"][i] = flat[at:at + sizes[i]]
-                    at += -(-sizes[i] // 8) * 8
         s["norm"] = new(1, dtype=torch.float32)
         if own:
             from chunk_scheduled_communication_gb300 import clip
@@ -190,11 +168,7 @@ def prepare(case, seed):
         s["dwg"], s["dwu"] = new(d, f, dtype=dt), new(d, f, dtype=dt)
     if own:
         from chunk_scheduled_communication_gb300 import ffn
-        s["plan"] = ffn.FfnPlan(d=d, d_ff=f, act=c["act"], dtype=c["dtype"], saved="fp32")
-        if c["op"] == "ffn_train":
-            # the projections are kept as they were computed, their gradients in the inputs' type
-            s["dg"], s["du"] = s["g"], s["u"]
-            s["g"], s["u"] = new(rows, f, dtype=torch.float32), new(rows, f, dtype=torch.float32)
+        s["plan"] = ffn.FfnPlan(d=d, d_ff=f, act=c["act"], dtype=c["dtype"])
     return s
 
 
@@ -247,10 +221,6 @@ def _plain_clip(s):
         total = total + t.float().square().sum(dtype=torch.float64)
     norm = total.sqrt()
     k = (s["case"]["max_norm"] / (norm + CLIP_EPS)).clamp(max=1.0).float()
-    if s["result"] is not s["out"]:
-        for t, o in zip(s["grads"], s["out"]):
-            torch.mul(t.float(), k, out=o)
-        return [norm.float().view(1)] + s["result"]
     return [norm.float().view(1)] + [(t.float() * k).to(t.dtype) for t in s["grads"]]
 
 
@@ -261,7 +231,7 @@ def run(state):
     plan = s["plan"]
     if c["op"] == "clip":
         plan.clip(s["grads"], c["max_norm"], s["norm"], out=s["out"], eps=CLIP_EPS)
-        return [s["norm"]] + s["result"]
+        return [s["norm"]] + s["out"]
     if c["op"] == "norm":
         plan.forward(s["x"], s["out"], s["w"], s["b"], eps=EPS)
         return s["out"]
@@ -272,7 +242,8 @@ def run(state):
         plan.forward(s["x"], s["wg"], s["wu"], s["h"])
         return s["h"]
     plan.forward(s["x"], s["wg"], s["wu"], s["h"], G=s["g"], U=s["u"])
-    plan.backward(s["dh"], s["x"], s["wg"], s["wu"], s["g"], s["u"], s["dg"], s["du"], s["dx"], s["dwg"], s["dwu"])
+    # in place: the gradients of the projections take the projections' place
+    plan.backward(s["dh"], s["x"], s["wg"], s["wu"], s["g"], s["u"], s["g"], s["u"], s["dx"], s["dwg"], s["dwu"])
     return s["h"], s["dx"], s["dwg"], s["dwu"]
 
 
@@ -283,7 +254,7 @@ def exact(case, seed):
         g = [t.double() for t in x["grads"]]
         norm = math.sqrt(sum(float(torch.dot(t, t)) for t in g))
         k = min(1.0, c["max_norm"] / (norm + CLIP_EPS))
-        return [torch.tensor([norm], dtype=torch.float64, device="cuda")] + _joined(c, [t * k for t in g])
+        return [torch.tensor([norm], dtype=torch.float64, device="cuda")] + [t * k for t in g]
     want = c["op"] in ("norm_grad", "ffn_train")
     if c["op"] in ("norm", "norm_grad"):
         t, w = x["x"].double().requires_grad_(want), x["w"].double().requires_grad_(want)
