@@ -116,3 +116,11 @@ def test_the_layer_keeps_its_projections_in_fp32(dtype):
     for got, inner, ref in zip(grads[2:], want[:2], want[2:]):
         error = ((got.double() - ref).norm() / ref.norm()).item()
         assert error <= 1.1 * math.hypot(step(inner), step(ref))
+
+
+def test_heads_that_make_rows_wider_than_the_norm_takes():
+    """The attention half runs all the same."""
+    r = window_layer.run(tokens=70, new=2, H_q=132, H_kv=4, width=40, sinks=2)
+    assert r["step"] is None and "step" not in r["ms"]
+    assert r["out"].shape[1:] == (132, 128) and all(r[k].isfinite().all() for k in ("out", "d_qkv", "dwq", "dwk"))
+    assert r["worst"] <= (2.0 ** -6 + 2.0 ** -13) * r["v_max"]
