@@ -137,8 +137,9 @@ __device__ __forceinline__ void raster(int t, int tiles_m, int tiles_n, int band
 // Waits are made by whole, converged warps, single-thread instructions by an elected
 // lane of theirs.
 //
-// A few polls without looking at the clock, each suspended for up to kSuspendNs: a
-// warp that polls without it takes the others' barrier operations time.  (The ring's
+// A few polls without looking at the clock, each suspended for up to kSuspendNs (4 us on
+// this GPU, whatever is asked: 80 us in all): a warp that polls without it takes the others'
+// barrier operations time.  (The ring's
 // barriers are completed by copies and products alone, which the barrier itself
 // orders before the products and copies behind it: no acquire at cluster scope.)
 constexpr uint32_t kSuspendNs = 20000;
@@ -184,10 +185,10 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
     if (!ok) ok = wait_long(bar, parity, abort, p);
     return __all_sync(0xffffffffu, ok);
 }
-// On the way out: ignores the abort flag, with a limit of its own
-__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, const Common &p) {
+// On the way out: ignores the abort flag, with a limit of its own from `since` on (0: now)
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, const Common &p, uint64_t since = 0) {
     if (!poll(bar, parity)) {
-        const uint64_t t0 = ptx::globaltimer(), limit = p.timeout_ns > window::kDrainNs ? p.timeout_ns : window::kDrainNs;
+        const uint64_t t0 = since != 0 ? since : ptx::globaltimer(), limit = p.timeout_ns > window::kDrainNs ? p.timeout_ns : window::kDrainNs;
         while (!poll(bar, parity))
             if (ptx::globaltimer() - t0 > limit) {
                 atomicCAS(p.err, 0, SYN_ERR_TIMEOUT);
@@ -325,10 +326,11 @@ template <class L, class Walk> __device__ __forceinline__ uint32_t produce(const
 // have landed before the pair leaves (else the products have waited for all of it).  Both
 // producers wake on the same commit, so one can be a use of a stage ahead of the other:
 // the even one arms the phases that only the odd one loads into (one that only the even
-// one loads into ends with the wait's limit).
+// one loads into ends with the limit, which counts once for all stages).
 template <class L> __device__ __forceinline__ void land(const Cta &c, uint32_t it, const Common &p) {
     volatile uint32_t *count = reinterpret_cast<volatile uint32_t *>(c.sm + L::OFF_MISC + 8), *bytes = count + 1;
-    drain(c.bar + 8 * L::PEER, 0, p);
+    const uint64_t since = ptx::globaltimer();
+    drain(c.bar + 8 * L::PEER, 0, p, since);
     (void)ptx::mbar_try_wait_cluster(c.bar + 8 * L::PEER, 0);  // (complete: acquires what the odd CTA wrote)
     const uint32_t other = *count, most = max(it, other);
     for (uint32_t k = 0; k < (uint32_t)L::S; ++k) {
@@ -337,7 +339,7 @@ template <class L> __device__ __forceinline__ void land(const Cta &c, uint32_t i
     }
     __syncwarp();
     for (uint32_t k = 0; k < (uint32_t)L::S; ++k)
-        if (most > k) drain(c.bar + 8 * (L::FULL + k), (((most - 1u - k) / L::S)) & 1u, p);
+        if (most > k) drain(c.bar + 8 * (L::FULL + k), (((most - 1u - k) / L::S)) & 1u, p, since);
 }
 
 // issued: the producer's k-blocks (warp 0)

@@ -49,7 +49,9 @@ typedef struct {
     int act;             /* SYN_ACT_*                                              */
     int backward;        /* 1: the plan can run syn_gated_ffn_backward             */
     int saved_f32;       /* 1: G and U are in fp32, 0: in dtype                    */
-    uint64_t timeout_ns; /* bound on every device wait (0 = SYN_TIMEOUT_NS or 2 s) */
+    uint64_t timeout_ns; /* bound on every device wait (0 = SYN_TIMEOUT_NS or 2 s); one that
+                            runs out is seen up to 0.2 ms later, and the call ends within
+                            the bound, at least a second, after that                    */
 } syn_ffn_cfg_t;
 
 /* A matrix: element (i, j) at p + i * row + j.  p 16-byte aligned; row (where
