@@ -166,6 +166,46 @@ int even_rounds(int pairs, int items1, int tiles2, int cost1, int cost2) {
     return best;
 }
 
+// A forward's tiles: columns of a product, rows and columns of tiles (n 0: too many), parts
+struct FwdTiles {
+    int width, m, n, split;
+};
+FwdTiles fwd_tiles(const syn_ffn_plan_s *pl, int64_t n_tokens) {
+    const syn_ffn_cfg_t &c = pl->cfg;
+    const int m = ceil_div(n_tokens, kTileM), wide = ceil_div(c.d_ff, 128), narrow = ceil_div(c.d_ff, 64);
+    if ((int64_t)m * narrow >= (int64_t)1 << 30) return {0, m, 0, 1};
+    // a round of narrow tiles takes 0.58 of one of wide ones (8 tokens: 3 rounds of narrow
+    // ones for 2; 1003 tokens, 3584 -> 2368: 1 of wide ones for 2)
+    const int64_t rounds_w = ceil_div((int64_t)m * wide, pl->pairs), rounds_n = ceil_div((int64_t)m * narrow, pl->pairs);
+    if (n_tokens > 64 && rounds_n * 58 >= rounds_w * 100) return {256, m, wide, 1};
+    return {128, m, narrow, parts_of(m * narrow, ceil_div(c.d, 128), pl->pairs, fwd_costs(n_tokens, c.d, c.d_ff))};
+}
+
+// The gradient's tiles of dX and of dW: those of the longer kind first, in parts
+constexpr int kEnd = 2;  // (stages that a tile's start and end cost, about)
+struct BwdDeal {
+    bool dw_first;
+    int n1, n2, stages1, stages2, split;
+};
+BwdDeal bwd_deal(const syn_ffn_plan_s *pl, int64_t n_tokens, int dx, int dw) {
+    const int tiles[2] = {dx, dw}, stages[2] = {2 * ceil_div(pl->cfg.d_ff, 128), ceil_div(n_tokens, 128)};
+    const bool first = dx == 0 || (dw > 0 && stages[1] > stages[0]);
+    BwdDeal t = {first, tiles[first], tiles[!first], stages[first], stages[!first], 1};
+    // the longer kind's tiles are cut where the pairs would wait for one of them
+    if (((int64_t)t.n1 * (t.stages1 + kEnd) + (int64_t)t.n2 * (t.stages2 + kEnd)) / pl->pairs < t.stages1 + kEnd)
+        t.split = parts_of(t.n1, t.stages1, pl->pairs, kBwdCosts);
+    return t;
+}
+int dx_tiles(const syn_ffn_plan_s *pl, int64_t n_tokens, int &m, int &n) {
+    m = ceil_div(n_tokens, kTileM);
+    n = ceil_div(pl->cfg.d, 256);
+    return (int64_t)m * n >= (int64_t)1 << 30 ? host_fail(SYN_ERR_UNSUPPORTED, "2^30 or more tiles") : SYN_OK;
+}
+void dw_tiles(const syn_ffn_plan_s *pl, int &m, int &n) {
+    m = ceil_div(pl->cfg.d, kTileM);
+    n = 2 * ceil_div(pl->cfg.d_ff, 256);
+}
+
 }  // namespace
 
 extern "C" {
@@ -231,6 +271,24 @@ int syn_ffn_plan_destroy(syn_ffn_plan_t pl) {
     return SYN_OK;
 }
 
+int syn_ffn_plan_parts(syn_ffn_plan_t pl, int64_t n_tokens, int want, int *forward, int *backward) {
+    int rc = check_call(pl, n_tokens);
+    if (rc != SYN_OK) return rc;
+    if (want < 0 || want > 3) return host_fail(SYN_ERR_INVALID, "want must be 0 to 3");
+    if (forward != nullptr) {
+        const FwdTiles t = n_tokens == 0 ? FwdTiles{0, 0, 1, 1} : fwd_tiles(pl, n_tokens);
+        if (t.n == 0) return host_fail(SYN_ERR_UNSUPPORTED, "2^30 or more tiles");
+        *forward = t.split;
+    }
+    if (backward != nullptr) {
+        int x[2] = {0, 0}, w[2] = {0, 0};
+        if ((want & 1) != 0 && (rc = dx_tiles(pl, n_tokens, x[0], x[1])) != SYN_OK) return rc;
+        if ((want & 2) != 0) dw_tiles(pl, w[0], w[1]);
+        *backward = want == 0 || n_tokens == 0 || !pl->cfg.backward ? 1 : bwd_deal(pl, n_tokens, x[0] * x[1], w[0] * w[1]).split;
+    }
+    return SYN_OK;
+}
+
 int syn_gated_ffn(syn_ffn_plan_t pl, const syn_ffn_mat_t *X, const syn_ffn_mat_t *Wg, const syn_ffn_mat_t *Wu,
                   const syn_ffn_mat_t *H, const syn_ffn_mat_t *G, const syn_ffn_mat_t *U, int64_t n_tokens, void *stream) {
     int rc = check_call(pl, n_tokens);
@@ -260,19 +318,16 @@ int syn_gated_ffn(syn_ffn_plan_t pl, const syn_ffn_mat_t *X, const syn_ffn_mat_t
     p.m = (int32_t)n_tokens;
     p.k = c.d;
     p.f = c.d_ff;
-    p.tiles_m = ceil_div(n_tokens, kTileM);
-    const int wide = ceil_div(c.d_ff, 128), narrow = ceil_div(c.d_ff, 64);
-    if ((int64_t)p.tiles_m * narrow >= (int64_t)1 << 30) return host_fail(SYN_ERR_UNSUPPORTED, "2^30 or more tiles");
-    // a round of narrow tiles takes 0.58 of one of wide ones (8 tokens: 3 rounds of narrow
-    // ones for 2; 1003 tokens, 3584 -> 2368: 1 of wide ones for 2)
-    const int64_t rounds_w = ceil_div((int64_t)p.tiles_m * wide, pl->pairs), rounds_n = ceil_div((int64_t)p.tiles_m * narrow, pl->pairs);
-    const int nt = n_tokens <= 64 || rounds_n * 58 < rounds_w * 100 ? 128 : 256;
-    p.tiles_n = nt == 256 ? wide : narrow;
+    const FwdTiles t = fwd_tiles(pl, n_tokens);
+    if (t.n == 0) return host_fail(SYN_ERR_UNSUPPORTED, "2^30 or more tiles");
+    const int nt = t.width;
+    p.tiles_m = t.m;
+    p.tiles_n = t.n;
     p.band = band_of(pl->pairs, p.tiles_m);
     p.x_rows = x_rows;
     p.keep = G == nullptr ? 0 : pl->wide ? 2 : 1;
     p.bf16 = pl->bf16;
-    p.split = nt == 128 ? parts_of(p.tiles_m * p.tiles_n, ceil_div(c.d, 128), pl->pairs, fwd_costs(n_tokens, c.d, c.d_ff)) : 1;
+    p.split = t.split;
     p.parts = pl->parts;
     FFN_CK(fwd_launch(c.act, nt, std::min(pl->pairs, p.tiles_m * p.tiles_n * p.split), p, m, static_cast<cudaStream_t>(stream)));
     return SYN_OK;
@@ -319,16 +374,13 @@ int syn_gated_ffn_backward(syn_ffn_plan_t pl, const syn_ffn_mat_t *dH, const syn
         if ((rc = encode(&m.wg, pl, *Wg, c.d, c.d_ff, false)) != SYN_OK || (rc = encode(&m.wu, pl, *Wu, c.d, c.d_ff, false)) != SYN_OK ||
             (rc = encode(&m.dx, pl, *dX, n_tokens, c.d, true)) != SYN_OK)
             return rc;
-        p.dx_m = ceil_div(n_tokens, kTileM);
-        p.dx_n = ceil_div(c.d, 256);
-        if ((int64_t)p.dx_m * p.dx_n >= (int64_t)1 << 30) return host_fail(SYN_ERR_UNSUPPORTED, "2^30 or more tiles");
+        if ((rc = dx_tiles(pl, n_tokens, p.dx_m, p.dx_n)) != SYN_OK) return rc;
     }
     if (dWg != nullptr) {
         if ((rc = encode(&m.x, pl, *X, n_tokens, c.d, false)) != SYN_OK || (rc = encode(&m.dwg, pl, *dWg, c.d, c.d_ff, true)) != SYN_OK ||
             (rc = encode(&m.dwu, pl, *dWu, c.d, c.d_ff, true)) != SYN_OK)
             return rc;
-        p.dw_m = ceil_div(c.d, kTileM);
-        p.dw_n = 2 * ceil_div(c.d_ff, 256);
+        dw_tiles(pl, p.dw_m, p.dw_n);
     }
     ActParams a;
     std::memset(&a, 0, sizeof(a));
@@ -346,19 +398,16 @@ int syn_gated_ffn_backward(syn_ffn_plan_t pl, const syn_ffn_mat_t *dH, const syn
     a.per_row = (uint32_t)(c.d_ff / 8);
     divisor(a.per_row, a.magic, a.shift);
     FFN_CK(act_grad_launch(c.act, pl->bf16, pl->wide, a, st));
-    const int tiles[2] = {p.dx_m * p.dx_n, p.dw_m * p.dw_n}, stages[2] = {2 * ceil_div(c.d_ff, 128), ceil_div(n_tokens, 128)};
-    if (tiles[0] + tiles[1] == 0) return SYN_OK;
-    // (a tile's start and end cost about two stages)
-    p.dw_first = tiles[0] == 0 || (tiles[1] > 0 && stages[1] > stages[0]);
-    const int n1 = tiles[p.dw_first], n2 = tiles[!p.dw_first], cost1 = stages[p.dw_first] + 2, cost2 = stages[!p.dw_first] + 2;
-    // the longer kind's tiles are cut where the pairs would wait for one of them
-    p.split = 1;
-    if (((int64_t)n1 * cost1 + (int64_t)n2 * cost2) / pl->pairs < cost1) p.split = parts_of(n1, stages[p.dw_first], pl->pairs, kBwdCosts);
+    if (p.dx_m * p.dx_n + p.dw_m * p.dw_n == 0) return SYN_OK;
+    const BwdDeal deal = bwd_deal(pl, n_tokens, p.dx_m * p.dx_n, p.dw_m * p.dw_n);
+    const int n1 = deal.n1, n2 = deal.n2;
+    p.dw_first = deal.dw_first;
+    p.split = deal.split;
     p.items1 = n1 * p.split;
     p.tiles2 = n2;
     p.parts = pl->parts;
     const int pairs = std::min(pl->pairs, p.items1 + p.tiles2);
-    p.even = even_rounds(pairs, p.items1, p.tiles2, stages[p.dw_first] / p.split + 2, cost2);
+    p.even = even_rounds(pairs, p.items1, p.tiles2, deal.stages1 / p.split + kEnd, deal.stages2 + kEnd);
     p.rest = p.items1 % pairs;
     p.band = band_of(pairs, std::max(p.dx_m, p.dw_m));
     FFN_CK(bwd_launch(pairs, p, m, st));

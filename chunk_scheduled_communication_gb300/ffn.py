@@ -34,6 +34,7 @@ SIGS = {
     "syn_ffn_cfg_default": (ctypes.c_int, [ctypes.POINTER(FfnCfg)]),
     "syn_ffn_plan_create": (ctypes.c_int, [ctypes.POINTER(_P), ctypes.POINTER(FfnCfg)]),
     "syn_ffn_plan_destroy": (ctypes.c_int, [_P]),
+    "syn_ffn_plan_parts": (ctypes.c_int, [_P, _I64, ctypes.c_int, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]),
     "syn_gated_ffn": (ctypes.c_int, [_P, _M, _M, _M, _M, _M, _M, _I64, _P]),
     "syn_gated_ffn_backward": (ctypes.c_int, [_P, _M, _M, _M, _M, _M, _M, _M, _M, _M, _M, _M, _I64, _P]),
     "syn_ffn_sync_status": (ctypes.c_int, [_P, _P]),
@@ -107,6 +108,13 @@ class FfnPlan:
 
     def _s(self, name, t, n):
         return None if t is None else _pack(*matrix_of(name, t, self.saved, n, self.cfg.d_ff, self._device))
+
+    def parts(self, tokens, dX=True, dW=True):
+        """Parts that the longer tiles of forward's and backward's products are cut into (1: whole)."""
+        forward, backward = ctypes.c_int(), ctypes.c_int()
+        _check(self._L.syn_ffn_plan_parts(self._h, tokens, int(dX) + 2 * int(dW), ctypes.byref(forward), ctypes.byref(backward)),
+               "syn_ffn_plan_parts")
+        return forward.value, backward.value
 
     def forward(self, X, Wg, Wu, H, G=None, U=None, stream=None):
         """H = act(X Wg) * (X Wu); G and U, which backward needs, where given."""

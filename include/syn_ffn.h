@@ -75,6 +75,11 @@ int syn_ffn_plan_create(syn_ffn_plan_t *out, const syn_ffn_cfg_t *cfg);
 /* Free a plan (no call of it may still be running).  NULL is a no-op. */
 int syn_ffn_plan_destroy(syn_ffn_plan_t plan);
 
+/* The parts that the longer tiles of a call's products are cut into where they are few (1:
+ * whole), of syn_gated_ffn and of syn_gated_ffn_backward with dX, with dWg and dWu, or with
+ * both (want: 1, 2, 3; 0: of neither).  Needs no GPU work; either result may be NULL. */
+int syn_ffn_plan_parts(syn_ffn_plan_t plan, int64_t n_tokens, int want, int *forward, int *backward);
+
 /* H (asynchronous on `stream`), and where they are not NULL the G and U that the
  * gradient needs.  Outputs overlap neither inputs nor each other.  The same bits for
  * the same inputs on the same device. */

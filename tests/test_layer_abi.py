@@ -95,3 +95,8 @@ def test_headers_compile_as_plain_c(tmp_path):
     r = subprocess.run([gcc, "-std=c11", "-Wall", "-Werror", "-fsyntax-only", "-I", os.path.join(ROOT, "include"), str(src)],
                        capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_parts_of_no_plan():
+    n = ctypes.c_int(7)
+    assert ffn.lib().syn_ffn_plan_parts(None, 1, 3, ctypes.byref(n), None) == syn.ERR_INVALID and n.value == 7
