@@ -326,3 +326,39 @@ def test_outputs_in_the_place_of_other_operands_are_refused():
         plan.backward(x, other, x, dw=f, db=torch.zeros_like(f))
         plan.backward(other, x, x, dw=f)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows, d, apart", [(8003, 777, 777), (9001, 777, 780), (20011, 333, 335), (5003, 1999, 1999), (3001, 4099, 4101)])
+def test_in_place_over_many_steps(rows, d, apart, dtype):
+    """Rows that begin at no 16-byte boundary, so many that blocks take them in steps: a row's
+    first and last vectors are read with a neighbour's elements beside them while that row is
+    written.  The same bits as in other tensors that lie alike, whose values are checked; what
+    lies between and around the rows stays."""
+    rng = np.random.default_rng(rows + d)
+    size = rows * apart + 16
+    part = lambda t: t.as_strided((rows, d), (apart, 1), 3)
+    flat = lambda: make(rng, size, dtype, 1.5, 0.3)
+    x, dy = flat(), flat()
+    w, b = make(rng, d, dtype, 0.2, 1.0), make(rng, d, dtype, 0.2)
+    keep = torch.ones(size, dtype=torch.bool, device="cuda")
+    part(keep).fill_(False)
+    sums = lambda: [torch.full((d,), 7.0, device="cuda") for _ in range(2)]
+    with norm.NormPlan(d=d, dtype=dtype) as plan:
+        y, dx, dsum = torch.zeros_like(x), torch.zeros_like(x), sums()
+        plan.forward(part(x), part(y), w, b)
+        plan.backward(part(x), part(dy), part(dx), w, *dsum)
+        x0, g0, w0 = f64(part(x)), f64(part(dy)), f64(w)
+        near(part(y), *forward(x0, w0, f64(b), 1e-5))
+        ref, tol, (rw, tw), (rb, tb) = backward(x0, g0, w0, 1e-5)
+        near(part(dx), ref, tol)
+        near(dsum[0], rw, tw)
+        near(dsum[1], rb, tb)
+        for _ in range(5):
+            over, over_dy, over_x, s1, s2 = x.clone(), dy.clone(), x.clone(), sums(), sums()
+            plan.forward(part(over), part(over), w, b)
+            plan.backward(part(x), part(over_dy), part(over_dy), w, *s1)
+            plan.backward(part(over_x), part(dy), part(over_x), w, *s2)
+            for got, want, before in ((over, y, x), (over_dy, dx, dy), (over_x, dx, x)):
+                assert torch.equal(part(got), part(want)) and torch.equal(got[keep], before[keep])
+            assert all(torch.equal(p, q) for s in (s1, s2) for p, q in zip(s, dsum))
