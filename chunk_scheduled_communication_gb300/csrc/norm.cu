@@ -42,7 +42,7 @@ using window::mul2;
 using window::unf2;
 
 constexpr int kMaxD = 16384;
-constexpr int kMaxGroups = 15;  // groups of several warps in a gradient block: barriers 1..15
+constexpr int kMaxGroups = 12;  // groups of several warps (64 lanes or more) in a block: barriers 1..12
 
 struct Args {
     const void *x, *dy;
@@ -428,6 +428,7 @@ template <typename T, int VEC> __device__ __forceinline__ void stage(Pack<T, VEC
 // weight and bias widened once), and one reduction a row, of its squares and the next
 // row's sum.
 constexpr int kRowThreads = 768, kRowElems = 16, kRowStages = 4;
+static_assert(kRowThreads / 64 <= kMaxGroups, "places and barriers of a block's groups");
 template <typename T, int VEC, bool EDGE>
 __global__ void __launch_bounds__(kRowThreads, 1) layer_norm_rows_kernel(const __grid_constant__ Args a) {
     constexpr int E = kRowElems, NV = E / VEC, TH = kRowThreads, S = kRowStages;
@@ -875,6 +876,7 @@ namespace {
     } while (0)
 
 constexpr int kGradThreads = 512;
+static_assert(kGradThreads <= kRowThreads, "places and barriers of a block's groups");
 constexpr int kRowSteps = 3;  // rows of a group at least, for the persistent forward
 constexpr int kGradElems = 16, kWideGradElems = 32;  // elements of a lane
 
@@ -930,7 +932,7 @@ int blocks_for(const syn_norm_plan_s *pl, const Args &a, int groups, bool edge, 
 
 template <typename T, int VEC, bool EDGE> int launch_rows(const syn_norm_plan_s *pl, Args &a, int n, cudaStream_t st) {
     a.lanes = lanes_for(n, kRowElems / VEC);
-    const int groups = a.lanes > 32 ? std::min(kRowThreads / a.lanes, kMaxGroups) : kRowThreads / a.lanes;
+    const int groups = kRowThreads / a.lanes;
     NORM_CK((window::launch_early(layer_norm_rows_kernel<T, VEC, EDGE>, (unsigned)blocks_for(pl, a, groups, EDGE, VEC),
                                   (unsigned)(groups * a.lanes), (size_t)(kRowStages * kRowElems * kRowThreads * (int)sizeof(T)), st, a)));
     return SYN_OK;
@@ -946,8 +948,9 @@ template <typename T, int VEC, bool EDGE> int forward_of(const syn_norm_plan_s *
         if (lanes_for(n, kRowElems / VEC) <= kRowThreads && a.rows * a.d >= (int64_t)pl->num_sms * kRowThreads * kRowElems * kRowSteps)
             return launch_rows<T, VEC, EDGE>(pl, a, n, st);
     if (a.rows * most <= (int64_t)pl->num_sms * 1024 && most <= 1024) return launch_forward<T, VEC, 1, EDGE>(a, n, st);
-    if (n <= 4096) return launch_forward<T, VEC, 4, EDGE>(a, n, st);
-    return launch_forward<T, VEC, (VEC > 1 ? 8 : 16), EDGE>(a, n, st);
+    if constexpr (VEC == 8) return launch_forward<T, VEC, 4, EDGE>(a, n, st);  // (2049 vectors at most)
+    else if (n <= 4096) return launch_forward<T, VEC, 4, EDGE>(a, n, st);
+    else return launch_forward<T, VEC, (VEC > 1 ? 8 : 16), EDGE>(a, n, st);
 }
 
 template <typename T> int forward_any(const syn_norm_plan_s *pl, Args &a, Access x, cudaStream_t st) {
@@ -959,8 +962,7 @@ template <typename T, int VEC, int E, int TH, bool EDGE>
 int launch_grad(const syn_norm_plan_s *pl, Args &a, int n, cudaStream_t st, int &grid) {
     constexpr int NV = E / VEC;
     a.lanes = lanes_for(n, NV);
-    int groups = TH / a.lanes;
-    if (a.lanes > 32) groups = std::min(groups, kMaxGroups);
+    const int groups = TH / a.lanes;
     grid = blocks_for(pl, a, groups, EDGE, VEC);
     NORM_CK((window::launch_early(layer_norm_grad_kernel<T, VEC, NV, TH, EDGE>, (unsigned)grid, (unsigned)(groups * a.lanes),
                                   (size_t)GradLay<T, VEC, NV, TH>::BYTES, st, a)));
