@@ -18,7 +18,8 @@ __device__ __forceinline__ float inverse(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// 1 / (1 + exp(-z)); to 1e-6 of itself (the exponential's error grows with |z|: 2^-24 |z|)
+// 1 / (1 + exp(-z)), to 2^-23 (8 + |z|) of itself: the exponential's argument is rounded, which
+// counts with its size (1e-6 at 1, 1e-5 at -80)
 __device__ __forceinline__ float sigmoid(float z) { return inverse(1.f + exp2_of(-1.4426950409f * z)); }
 
 // The tanh form is g * sigmoid(2 sqrt(2/pi) (g + 0.044715 g^3)); g is held within

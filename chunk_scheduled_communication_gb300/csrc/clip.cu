@@ -96,7 +96,9 @@ template <typename T> struct Vec {
 
 // Sum of squares of a thread's vectors from `at` on, where they leave fp32's range:
 // the elements are scaled by a power of two that brings the largest to about one.
-// (Out of line: it is rare, and inline its registers cost the loop's blocks.)
+// (Out of line: inline its registers cost the loop's blocks.  Vectors of zeros come here
+// too and are read a second time: the norm of 176 million takes 113 us in fp32 for 104 of
+// other values, 64 for 56 in bf16.)
 template <typename T> __device__ __noinline__ double scaled_squares(const uint4 *q, int at, int end) {
     constexpr int N = Vec<T>::N;
     float top = 0.f;

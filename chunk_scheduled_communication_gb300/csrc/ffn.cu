@@ -130,6 +130,10 @@ struct Costs {
 Costs fwd_costs(int64_t n_tokens, int d, int d_ff) {
     return {0.3 + (n_tokens > 16 && d % 16 != 0 ? 0.12 : 0.0) + (d_ff % 16 != 0 ? 0.12 : 0.0), 2.9, 1.0, 0.015};
 }
+// (The gradient, dX and dW, whole tiles against this rule's parts: 120 tokens, 512 -> 14400
+// 147 us, 42 in 12 parts; 200, 1024 -> 8192 86, 37 in 8; 9000, 264 -> 520 63, 39.5 in 4;
+// 30000, 512 -> 512 167, 77 in 7; 128, 4096 -> 14336 162, 106 in 4; 2116, 312 -> 2920 48, 42
+// in 2; but 277, 4024 -> 6808 89.6, 92.2 in 2.)
 constexpr Costs kBwdCosts = {0.6, 0.0, 0.5, 0.25};
 
 // Parts of each of `tiles` tiles of `stages` stages, where they leave pairs without

@@ -21,11 +21,11 @@
 // says which it is.
 //
 // What bounds it, measured on one GB300: at 256 x 256 tiles the tensor pipe, 512 cycles a
-// k-block of 64 (8192 tokens, 4096 -> 14336: 966-990 us in short runs, 1.99 PFLOP/s, and
-// 1030-1150 in long ones, under the power cap), once the products' warp needs less than
+// k-block of 64 (8192 tokens, 4096 -> 14336: 959-990 us in short runs, 1.99 PFLOP/s, and
+// 1030-1150 in long ones, 1.70, under the power cap), once the products' warp needs less than
 // that for its wait, its products and its commit: one diverged lane took 630 cycles for
 // them, converged warps 620, an elected lane 500, two k-blocks a stage 320.  With few
-// tokens the weights' bytes bound it (8 tokens: 40-42 us, 35 of them HBM's).  Where a tile
+// tokens the weights' bytes bound it (8 tokens: 40-43 us, 35 of them HBM's).  Where a tile
 // has few k-blocks its end does, 1.8 us (SiLU) to 2.3 (GELU) at 256 x 256: 19456 tokens,
 // 128 -> 1280 21.3 us, ten tiles a pair.
 #pragma once
@@ -139,9 +139,9 @@ __device__ __forceinline__ void raster(int t, int tiles_m, int tiles_n, int band
 //
 // A few polls without looking at the clock, each suspended for up to kSuspendNs (4 us on
 // this GPU, whatever is asked: 80 us in all): a warp that polls without it takes the others'
-// barrier operations time.  (The ring's
-// barriers are completed by copies and products alone, which the barrier itself
-// orders before the products and copies behind it: no acquire at cluster scope.)
+// barrier operations time.  (The ring's barriers are completed by copies and products
+// alone, which the barrier itself orders before the products and copies behind it: no
+// acquire at cluster scope.)
 constexpr uint32_t kSuspendNs = 20000;
 __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
     uint32_t ok;

@@ -18,7 +18,7 @@ int host_load_driver();
 // elements, boxes of box_cols x box_rows.
 int host_encode_2d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, int esize, uint64_t cols,
                    uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz);
-// The same over a matrix of 16-bit elements whose rows are row_bytes apart.
+// The same over a matrix whose rows are row_bytes apart.
 int host_encode_rows(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint64_t cols, uint64_t rows,
                      uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz);
 // 3-D tiled tensor map over [rows, heads, cols] with row and head strides in

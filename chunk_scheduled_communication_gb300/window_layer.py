@@ -1,7 +1,9 @@
-"""A decoder layer from the library's operators: the attention half (head norm and
-rotation, windowed attention with sinks, their gradients, decoding over a paged
-cache) and the feed-forward half (layer norm, gated block, their gradients), with
-the clipping of all their gradients.
+"""The operators of a decoder layer's halves in training and serving: the attention
+half (head norm and rotation, windowed attention with sinks, their gradients,
+decoding over a paged cache) and the feed-forward half (layer norm, gated block,
+their gradients), with the clipping of all their gradients.  The output and down
+projections and the residual sums of a whole layer are not part of it: the
+attention's rows go into the layer norm as they are.
 
     python -m chunk_scheduled_communication_gb300.window_layer --tokens 1000 --new 16
 
@@ -99,8 +101,8 @@ class FeedForward:
 
 
 def train_step(layer, feed, clipping, plan, qkv, positions, d_h, max_norm):
-    """One training step of both halves: the feed-forward half's rows, the gradient of
-    qkv, the weights' gradients (of the head norms, the layer norm's w and b, the
+    """One training step of both halves, the attention's rows going into the layer norm as
+    they are: the feed-forward half's rows, the gradient of qkv, the weights' gradients (of the head norms, the layer norm's w and b, the
     block's wg and wu) clipped in place, and their norm."""
     out, saved = layer.forward(plan, qkv, positions)
     h, kept = feed.forward(out.flatten(1))

@@ -12,8 +12,9 @@
  * Precision: squares and short sums in fp32, scaled where they would leave its
  * range, so that every finite input has its norm (inf only above fp32's largest);
  * longer sums in fp64, in a fixed order: the same bits for the same inputs on the
- * same device.  c is computed in fp64 and rounded to fp32, a product is rounded
- * once to the tensor's type.  An element that is NaN makes the norm, c and all y
+ * same device.  c is computed in fp64 and rounded to fp32; a product is rounded to
+ * fp32 and then to the tensor's type (one below fp32's smallest normal number once
+ * more).  An element that is NaN makes the norm, c and all y
  * NaN; one that is infinite makes the norm infinite and c 0 (with
  * max_norm infinite too, NaN): the caller reads the norm to tell.
  */
